@@ -7,6 +7,7 @@ when it is missing.
 """
 from .api import attention_bwd, attention_decode, attention_fwd, bwd_workspace, check, dropout_mask
 from .autograd import FlashAttentionFunction, flash_attention
+from .paged import attention_paged, kv_append, paged_workspace, rope_tables
 
 __all__ = ["attention_fwd", "attention_bwd", "attention_decode", "bwd_workspace", "check", "dropout_mask", "flash_attention",
-           "FlashAttentionFunction"]
+           "FlashAttentionFunction", "attention_paged", "kv_append", "paged_workspace", "rope_tables"]

@@ -9,12 +9,13 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfa_sm100.so")
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_INTERNAL = range(6)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_INTERNAL, FA_ERR_RANGE = range(7)
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
-                4: "FA_ERR_TIMEOUT", 5: "FA_ERR_INTERNAL"}
+                4: "FA_ERR_TIMEOUT", 5: "FA_ERR_INTERNAL", 6: "FA_ERR_RANGE"}
 
 # name -> (restype, argtypes)
 _P, _I, _F, _U64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64, ctypes.c_size_t
+_I64, _SIZES = ctypes.c_int64, [_I] * 8   # B, Hq, Hkv, Nq, d, n_pages, page_size, max_pages
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _F, _U64, _P]),
     "fa_fwd_f32": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _F, _U64, _P]),
@@ -29,6 +30,11 @@ SIGNATURES = {
     "fa_fwd_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_fwd_decode_split": (_I, [_I, _I, _I, _I]),
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _SZ, _P]),
+    "fa_kv_append": (_I, [_P] * 7 + [_I64, _I64] + [_P] * 5 + [_I, _I, _I] + _SIZES + [_P]),
+    "fa_kv_append_e4m3": (_I, [_P] * 9 + [_I64, _I64] + [_P] * 5 + [_I, _I, _I] + _SIZES + [_P]),
+    "fa_fwd_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_fwd_paged": (_I, [_P] * 5 + [_I64, _I64] + [_P] * 3 + _SIZES + [_F, _I, _P, _SZ, _P]),
+    "fa_fwd_paged_e4m3": (_I, [_P] * 7 + [_I64, _I64] + [_P] * 3 + _SIZES + [_F, _I, _P, _SZ, _P]),
     "fa_bwd_head_group": (_I, [_I, _I, _SZ]),
     "fa_dropout_mask": (_I, [_P, _I, _I, _I, _F, _U64, _P]),
     "fa_test_exp2_fma": (_I, [_P, _P, _I, _P]),

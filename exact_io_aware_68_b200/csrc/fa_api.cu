@@ -19,6 +19,8 @@
 #include "decode_sm100.cuh"
 #include "fwd256_sm100.cuh"
 #include "fwd_sm100.cuh"
+#include "kv_append.cuh"
+#include "paged_sm100.cuh"
 #include "simt_f32.cuh"
 
 namespace {
@@ -417,6 +419,253 @@ fa_status fwd256(const void* q, const void* k, const void* v, void* o, float* ls
   return launch_status("fa_fwd (d = 256) kernel launch");
 }
 
+// ----------------------------------------------------------------------------- paged cache
+// What the append and the attention check alike; d = 64 or 128 keeps a row a whole number of threads
+// and of swizzled chunks, a page of 16 keys or more keeps an MMA's 16 keys inside one page.
+fa_status check_paged(int B, int Hq, int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages,
+                      int64_t k_page_stride, int64_t v_page_stride) {
+  if (B < 1 || Hkv < 1 || Nq < 1 || n_pages < 1 || max_pages < 1)
+    return fail(FA_ERR_INVALID_ARG, "B, Hkv, Nq, n_pages and max_pages must be >= 1 (got %d, %d, %d, %d, %d)", B, Hkv, Nq,
+                n_pages, max_pages);
+  if (Hq < 1 || Hq % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "Hq = %d must be a positive multiple of Hkv = %d", Hq, Hkv);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dimension d = %d: the paged cache supports d in {64, 128}", d);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+    return fail(FA_ERR_UNSUPPORTED, "page_size = %d: 16, 32, 64, 128 or 256", page_size);
+  if (B > fa::kPagedMaxB) return fail(FA_ERR_UNSUPPORTED, "B = %d exceeds %d", B, fa::kPagedMaxB);
+  if (int64_t(B) * Hq > 65535) return fail(FA_ERR_UNSUPPORTED, "B*Hq = %lld exceeds 65535", (long long)B * Hq);
+  if (Nq > (1 << 20)) return fail(FA_ERR_UNSUPPORTED, "Nq = %d is too large", Nq);
+  if (int64_t(B) * max_pages * page_size >= (int64_t(1) << 31))
+    return fail(FA_ERR_UNSUPPORTED, "B * max_pages * page_size = %lld must be below 2^31", (long long)B * max_pages * page_size);
+  const int64_t page = int64_t(Hkv) * page_size * d;
+  for (const int64_t s : {k_page_stride, v_page_stride})
+    if (s < page || s % 16 != 0)
+      return fail(FA_ERR_INVALID_ARG, "page stride %lld must be a multiple of 16, at least Hkv * page_size * d = %lld",
+                  (long long)s, (long long)page);
+  return FA_OK;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// Rows of one K/V head's row tile: 8 while its rows fit (the MMA's other 8 rows then carry the
+// probabilities' low halves), else 16.
+int paged_row_tile(int R) { return R <= 8 ? 8 : 16; }
+// The grid of the split kernel: one CTA per SM; with no device a bound for any.
+int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
+size_t paged_slots(int sms) { return size_t(paged_ctas(sms)) * fa::kPagedWarps * 2; }
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+size_t paged_ws_bytes(int B, int R, int d, int sms) {
+  const size_t rows = paged_slots(sms) * paged_row_tile(R);
+  return up256(rows * d * 4) + up256(rows * 8) + up256(size_t(B + 1) * 4);
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream: the kernel may be
+// scheduled early and waits (griddepcontrol.wait) until that grid has completed.
+template <typename P>
+fa_status launch_dependent(void (*kernel)(P), dim3 grid, dim3 block, const P& p, cudaStream_t s, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return launch_status(what);
+}
+
+template <int D, bool FP8, bool R16>
+fa_status launch_paged(fa::PagedParams p, int sms, cudaStream_t s) {
+  using Lt = fa::PagedLayout<D, FP8>;
+  constexpr int RT = R16 ? 16 : 8;
+  const int ctas = paged_ctas(sms);
+  p.n_warps = ctas * fa::kPagedWarps;
+  p.row_tiles = (p.R + RT - 1) / RT;
+  fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, R16>, Lt::bytes(fa::kPagedMaxB));
+  if (st != FA_OK) return st;
+  fa::fa_paged_split_kernel<D, FP8, R16><<<ctas, 32 * fa::kPagedWarps, Lt::bytes(p.B), s>>>(p);
+  if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
+  const long long rows = (long long)p.B * p.Hkv * p.R;
+  // A row tile has about n_warps / (B Hkv row_tiles) partials: one warp merges a row up to 8 of them, else a CTA
+  if ((long long)p.n_warps > 8LL * p.B * p.Hkv * p.row_tiles)
+    return launch_dependent(fa::fa_paged_combine_kernel<D, RT, 8>, dim3(unsigned(rows)), dim3(256), p, s,
+                            "fa_fwd_paged combine kernel launch");
+  return launch_dependent(fa::fa_paged_combine_kernel<D, RT, 1>, dim3(unsigned((rows + 7) / 8)), dim3(256), p, s,
+                          "fa_fwd_paged combine kernel launch");
+}
+
+fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, void* o, float* lse, int64_t k_page_stride, int64_t v_page_stride,
+                    const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens, int B, int Hq, int Hkv,
+                    int Nq, int d, int n_pages, int page_size, int max_pages, float scale, int causal, void* workspace,
+                    size_t workspace_bytes, cudaStream_t s) {
+  fa_status st = check_paged(B, Hq, Hkv, Nq, d, n_pages, page_size, max_pages, k_page_stride, v_page_stride);
+  if (st != FA_OK) return st;
+  if (int64_t(B) * Hq * Nq >= (int64_t(1) << 31))
+    return fail(FA_ERR_UNSUPPORTED, "B * Hq * Nq = %lld must be below 2^31", (long long)B * Hq * Nq);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  FA_CHECK_PTR(q);
+  FA_CHECK_PTR(k_cache);
+  FA_CHECK_PTR(v_cache);
+  FA_CHECK_PTR(o);
+  FA_CHECK_PTR(lse);
+  FA_CHECK_PTR(page_table);
+  FA_CHECK_PTR(key_lens);
+  if (fp8) {
+    FA_CHECK_PTR(k_scale);
+    FA_CHECK_PTR(v_scale);
+  }
+  if (workspace == nullptr) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(FA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  int sms = 0;
+  const int R = Hq / Hkv * Nq;
+  const size_t least = paged_ws_bytes(B, R, d, 1);   // refused without a device too
+  if (workspace_bytes < least) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs more than %zu", workspace_bytes, least);
+  if ((st = sm_count(&sms)) != FA_OK) return st;
+  const size_t need = paged_ws_bytes(B, R, d, sms);
+  if (workspace_bytes < need) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t rows = paged_slots(sms) * paged_row_tile(R);
+  fa::PagedParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const uint8_t*>(k_cache);
+  p.v = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + up256(rows * d * 4));
+  p.plan = reinterpret_cast<int*>(ws + up256(rows * d * 4) + up256(rows * 8));
+  p.page_table = page_table;
+  p.key_lens = key_lens;
+  p.new_lens = new_lens;
+  p.k_page_bytes = k_page_stride * (fp8 ? 1 : 2);
+  p.v_page_bytes = v_page_stride * (fp8 ? 1 : 2);
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.R = R;
+  p.n_pages = n_pages;
+  p.page_shift = log2_of(page_size);
+  p.max_pages = max_pages;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const bool wide = paged_row_tile(R) == 16;
+  if (d == 64) {
+    if (fp8) return wide ? launch_paged<64, true, true>(p, sms, s) : launch_paged<64, true, false>(p, sms, s);
+    return wide ? launch_paged<64, false, true>(p, sms, s) : launch_paged<64, false, false>(p, sms, s);
+  }
+  if (fp8) return wide ? launch_paged<128, true, true>(p, sms, s) : launch_paged<128, true, false>(p, sms, s);
+  return wide ? launch_paged<128, false, true>(p, sms, s) : launch_paged<128, false, false>(p, sms, s);
+}
+
+fa_status run_append(bool fp8, const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
+                     void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t k_page_stride,
+                     int64_t v_page_stride, const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
+                     const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim, int interleaved, int B, int Hq,
+                     int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages, cudaStream_t s) {
+  fa_status st = check_paged(B, q == nullptr ? Hkv : Hq, Hkv, Nq, d, n_pages, page_size, max_pages, k_page_stride, v_page_stride);
+  if (st != FA_OK) return st;
+  FA_CHECK_PTR(k);
+  FA_CHECK_PTR(v);
+  if (q != nullptr) {
+    FA_CHECK_PTR(q);
+    FA_CHECK_PTR(q_out);
+  }
+  FA_CHECK_PTR(k_cache);
+  FA_CHECK_PTR(v_cache);
+  if (fp8) {
+    FA_CHECK_PTR(k_scale);
+    FA_CHECK_PTR(v_scale);
+  }
+  FA_CHECK_PTR(page_table);
+  FA_CHECK_PTR(key_lens);
+  if (strides == nullptr) return fail(FA_ERR_INVALID_ARG, "strides is NULL");
+  for (int i = q == nullptr ? 3 : 0; i < 9; ++i)
+    if (strides[i] < 0 || strides[i] % 8 != 0)
+      return fail(FA_ERR_INVALID_ARG, "strides[%d] = %lld must be a multiple of 8, >= 0", i, (long long)strides[i]);
+  if ((rope_cos == nullptr) != (rope_sin == nullptr)) return fail(FA_ERR_INVALID_ARG, "rope_cos and rope_sin go together");
+  if (rope_cos != nullptr) {
+    FA_CHECK_PTR(rope_cos);
+    FA_CHECK_PTR(rope_sin);
+    if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0)
+      return fail(FA_ERR_UNSUPPORTED, "rot_dim = %d: a multiple of 16, at most d = %d", rot_dim, d);
+    if (max_pos < 1) return fail(FA_ERR_INVALID_ARG, "max_pos = %d must be >= 1", max_pos);
+  }
+  fa::AppendParams p{};
+  const void* x[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    p.x[i] = static_cast<const __nv_bfloat16*>(x[i]);
+    p.sb[i] = strides[3 * i];
+    p.sh[i] = strides[3 * i + 1];
+    p.sn[i] = strides[3 * i + 2];
+  }
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.pool[0] = static_cast<uint8_t*>(k_cache);
+  p.pool[1] = static_cast<uint8_t*>(v_cache);
+  p.page_bytes[0] = k_page_stride * (fp8 ? 1 : 2);
+  p.page_bytes[1] = v_page_stride * (fp8 ? 1 : 2);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.page_table = page_table;
+  p.key_lens = key_lens;
+  p.new_lens = new_lens;
+  p.cos = rope_cos;
+  p.sin = rope_sin;
+  p.B = B;
+  p.Hq = q == nullptr ? 0 : Hq;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.d = d;
+  p.rot = rope_cos == nullptr ? 0 : rot_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  p.max_pos = max_pos;
+  p.n_pages = n_pages;
+  p.page_shift = log2_of(page_size);
+  p.max_pages = max_pages;
+  const int heads = p.Hq + (fp8 ? 0 : 2 * Hkv);
+  const int64_t tokens = int64_t(B) * Nq;
+  // the row role's blocks hold `threads` threads of d / 16 per token; a thread takes up to 8 heads of its token
+  // as long as that leaves about 2048 threads per SM
+  auto rows = [&](int threads) {
+    const int per = threads / (d / 16);
+    p.row_blocks_x = int((tokens + per - 1) / per);
+    p.heads_per_thread = 1;
+    while (p.heads_per_thread < 8 && tokens * (d / 16) * heads / (2 * p.heads_per_thread) >= 148 * 2048) p.heads_per_thread *= 2;
+    p.row_blocks = heads == 0 ? 0 : p.row_blocks_x * ((heads + p.heads_per_thread - 1) / p.heads_per_thread);
+  };
+  if (!fp8) {
+    rows(128);
+    fa::fa_kv_append_kernel<<<p.row_blocks, 128, 0, s>>>(p);
+    return launch_status("fa_kv_append kernel launch");
+  }
+  p.touched = (Nq + page_size - 2) / page_size + 1;
+  const int most = Nq < page_size ? Nq : page_size;   // new rows of one page
+  const int lpr = d / 16;
+  int threads = 32;
+  while (threads / lpr * 4 < most) threads *= 2;
+  rows(threads);
+  const int64_t blocks = p.row_blocks + int64_t(B) * p.touched * Hkv * 2;
+  if (blocks >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "too many pages to append to (%lld)", (long long)blocks);
+  const unsigned grid = unsigned(blocks);
+  switch (threads) {
+    case 32: fa::fa_kv_append_e4m3_kernel<32><<<grid, 32, 0, s>>>(p); break;
+    case 64: fa::fa_kv_append_e4m3_kernel<64><<<grid, 64, 0, s>>>(p); break;
+    case 128: fa::fa_kv_append_e4m3_kernel<128><<<grid, 128, 0, s>>>(p); break;
+    case 256: fa::fa_kv_append_e4m3_kernel<256><<<grid, 256, 0, s>>>(p); break;
+    default: fa::fa_kv_append_e4m3_kernel<512><<<grid, 512, 0, s>>>(p); break;
+  }
+  return launch_status("fa_kv_append_e4m3 kernel launch");
+}
+
 unsigned grid_for(uint64_t work, unsigned per_block) {
   const uint64_t g = (work + per_block - 1) / per_block;
   return unsigned(g < 1 ? 1 : (g > (1u << 30) ? (1u << 30) : g));
@@ -718,6 +967,51 @@ fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void* o, fl
   return d == 64 ? launch_decode<64>(mq, mk, mv, p, stream) : launch_decode<128>(mq, mk, mv, p, stream);
 }
 
+size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || d < 1 || B > fa::kPagedMaxB) return 0;
+  if (int64_t(B) * Hq * Nq >= (int64_t(1) << 31)) return 0;
+  return paged_ws_bytes(B, Hq / Hkv * Nq, d, decode_sms());
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, int64_t k_page_stride,
+                       int64_t v_page_stride, const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
+                       int B, int Hq, int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages, float scale,
+                       int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return run_paged(false, q, k_cache, v_cache, nullptr, nullptr, o, lse, k_page_stride, v_page_stride, page_table, key_lens,
+                   new_lens, B, Hq, Hkv, Nq, d, n_pages, page_size, max_pages, scale, causal, workspace, workspace_bytes,
+                   stream);
+}
+
+fa_status fa_fwd_paged_e4m3(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, void* o, float* lse, int64_t k_page_stride, int64_t v_page_stride,
+                            const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens, int B, int Hq,
+                            int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages, float scale, int causal,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return run_paged(true, q, k_cache, v_cache, k_scale, v_scale, o, lse, k_page_stride, v_page_stride, page_table, key_lens,
+                   new_lens, B, Hq, Hkv, Nq, d, n_pages, page_size, max_pages, scale, causal, workspace, workspace_bytes,
+                   stream);
+}
+
+fa_status fa_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, void* q_out, void* k_cache,
+                       void* v_cache, int64_t k_page_stride, int64_t v_page_stride, const int32_t* page_table,
+                       const int32_t* key_lens, const int32_t* new_lens, const float* rope_cos, const float* rope_sin,
+                       int max_pos, int rot_dim, int interleaved, int B, int Hq, int Hkv, int Nq, int d, int n_pages,
+                       int page_size, int max_pages, cudaStream_t stream) {
+  return run_append(false, q, k, v, strides, q_out, k_cache, v_cache, nullptr, nullptr, k_page_stride, v_page_stride,
+                    page_table, key_lens, new_lens, rope_cos, rope_sin, max_pos, rot_dim, interleaved, B, Hq, Hkv, Nq, d,
+                    n_pages, page_size, max_pages, stream);
+}
+
+fa_status fa_kv_append_e4m3(const void* q, const void* k, const void* v, const int64_t* strides, void* q_out, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, int64_t k_page_stride, int64_t v_page_stride,
+                            const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
+                            const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim, int interleaved, int B,
+                            int Hq, int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages, cudaStream_t stream) {
+  return run_append(true, q, k, v, strides, q_out, k_cache, v_cache, k_scale, v_scale, k_page_stride, v_page_stride,
+                    page_table, key_lens, new_lens, rope_cos, rope_sin, max_pos, rot_dim, interleaved, B, Hq, Hkv, Nq, d,
+                    n_pages, page_size, max_pages, stream);
+}
+
 fa_status fa_dropout_mask(uint8_t* keep, int B, int H, int N, float dropout_p, uint64_t seed, cudaStream_t stream) {
   if (keep == nullptr) return fail(FA_ERR_INVALID_ARG, "keep is NULL");
   if (B < 1 || H < 1 || N < 1) return fail(FA_ERR_INVALID_ARG, "B, H and N must be >= 1");
@@ -751,6 +1045,8 @@ fa_status fa_check(cudaStream_t stream) {
   e = cudaMemcpyToSymbol(fa::g_fa_device_status, &zero, sizeof(int));
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "clearing the device status word: %s", cudaGetErrorString(e));
   if (code == fa::kStatusTimeout) return fail(FA_ERR_TIMEOUT, "a kernel's bounded wait ran out");
+  if (code == fa::kStatusRange)
+    return fail(FA_ERR_RANGE, "a page number, length or position was outside the paged cache");
   return fail(FA_ERR_INTERNAL, "device status %d (dynamic shared memory not 1024-byte aligned)", code);
 }
 

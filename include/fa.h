@@ -62,7 +62,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,  /* a valid request this build does not implement (e.g. bf16 with d = 96) */
   FA_ERR_CUDA = 3,         /* a CUDA runtime or driver call failed */
   FA_ERR_TIMEOUT = 4,      /* a kernel's bounded wait ran out; its outputs are undefined */
-  FA_ERR_INTERNAL = 5      /* the device reported an inconsistent launch (e.g. shared memory alignment) */
+  FA_ERR_INTERNAL = 5,     /* the device reported an inconsistent launch (e.g. shared memory alignment) */
+  FA_ERR_RANGE = 6         /* the device met a page number, length or position outside the paged cache */
 } fa_status;
 
 /* Forward, bf16 ("48 FlashAttention", block "Tiling и online softmax": tile by tile with a running
@@ -171,6 +172,82 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
                         const int32_t* key_lens, void* workspace, size_t workspace_bytes,
                         cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Paged key/value cache: keys and values of all sequences in pages of one pool, for serving
+ * ("48 FlashAttention", block "Связи": the attention under vLLM / PagedAttention).
+ *
+ *  - Pools: k_cache and v_cache are [n_pages, Hkv, page_size, d], the last three dimensions
+ *    contiguous, consecutive pages k_page_stride / v_page_stride elements apart (a multiple of 16, at
+ *    least Hkv * page_size * d; larger where one allocation holds several pools).  bf16, or e4m3 with
+ *    one fp32 scale per page and head: k_scale, v_scale [n_pages, Hkv]; a stored code c means c * scale.
+ *    Scales are finite and > 0.  page_size in {16, 32, 64, 128, 256}; d in {64, 128}.
+ *  - page_table: int32 [B, max_pages].  Key j of sequence b is row j % page_size of page
+ *    page_table[b][j / page_size].  Entries past a sequence's last key are not read.  Pages may be
+ *    shared by sequences, except those that an append writes.
+ *  - key_lens: int32 [B], the keys that sequence b holds AFTER the append of this step; new_lens: int32
+ *    [B] or NULL (all Nq), how many of the step's Nq tokens are real, 0 <= new_lens[b] <= Nq.  New token
+ *    i of sequence b stands at position key_lens[b] - new_lens[b] + i.  The same two arrays go to the
+ *    append and to the attention.
+ *  - Grouped heads: query head h uses K/V head h / (Hq / Hkv); Hq must be a multiple of Hkv.
+ *  - 1 <= B <= 4096, B * Hq <= 65535, and B * max_pages * page_size < 2^31.
+ *  - What the device finds out of range (a page number outside [0, n_pages), key_lens outside
+ *    [0, max_pages * page_size], new_lens outside [0, Nq], an append before position 0 or past the
+ *    rotation tables) is not accessed; fa_check() then returns FA_ERR_RANGE, and the outputs of
+ *    that sequence are undefined.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Appends the new keys and values to the pool, rotating keys (and queries) by their positions.
+ * q, k, v: bf16 [B, Hq | Hkv | Hkv, Nq, d] with d contiguous; strides: HOST array of nine element strides
+ * (batch, head, token of q, then k, then v), multiples of 8, so that views of one projection output need
+ * no copy.  q may be NULL (then q_out is not written); q_out: bf16 [B, Hq, Nq, d] contiguous, rows of
+ * queries that are no token (i >= new_lens[b]) are set to 0.  Rows of the pool that get no token keep
+ * their bytes.
+ * Rotation: rope_cos, rope_sin fp32 [max_pos, rot_dim / 2], both NULL for none; rot_dim a multiple of
+ * 16, at most d; features past rot_dim pass through.  Pair (x, y) becomes (x cos - y sin,
+ * y cos + x sin) in fp32, products rounded before the sum, pairs (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * with interleaved != 0.  One kernel launch. */
+FA_API fa_status fa_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
+                       void* k_cache, void* v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                       const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
+                       const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim, int interleaved,
+                       int B, int Hq, int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages,
+                       cudaStream_t stream);
+
+/* The same into e4m3 pools.  The scale of a page and head that gets new tokens becomes max(s, 2^e): 2^e
+ * the smallest power of two (at least 2^-117) with |x| <= 448 * 2^e over the page's new finite values
+ * (rotated, in fp32), s the page's scale if it held earlier tokens of the sequence (else none).  Where that
+ * raises the scale, the earlier tokens' codes are re-rounded by s / (new scale).  Codes are rounded to
+ * nearest even; infinities saturate, NaN stays NaN.  A page must belong to one sequence only.
+ * One kernel launch. */
+FA_API fa_status fa_kv_append_e4m3(const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
+                            void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            int64_t k_page_stride, int64_t v_page_stride,
+                            const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
+                            const float* rope_cos, const float* rope_sin, int max_pos, int rot_dim, int interleaved,
+                            int B, int Hq, int Hkv, int Nq, int d, int n_pages, int page_size, int max_pages,
+                            cudaStream_t stream);
+
+/* Attention of Nq >= 1 new queries per head to the keys of their sequences in the pool.
+ * q: bf16 [B, Hq, Nq, d] contiguous; writes o (bf16, the same shape) and lse (fp32 [B, Hq, Nq]).  Query i
+ * of sequence b sees keys j < key_lens[b], and with causal != 0 only j <= key_lens[b] - new_lens[b] + i.
+ * A query with no key, and one that is no token (i >= new_lens[b]), gets O = 0 and lse = -inf.
+ * workspace: at least fa_fwd_paged_workspace_size() bytes (of the current device; with no visible
+ * device a size that is enough on any), 256-byte aligned, clobbered; not shared by calls that may
+ * overlap.  Its size does not depend on the sequences' lengths.  Two kernel launches. */
+FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+FA_API fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                       int64_t k_page_stride, int64_t v_page_stride, const int32_t* page_table,
+                       const int32_t* key_lens, const int32_t* new_lens, int B, int Hq, int Hkv, int Nq, int d,
+                       int n_pages, int page_size, int max_pages, float scale, int causal,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* The same over e4m3 pools. */
+FA_API fa_status fa_fwd_paged_e4m3(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, void* o, float* lse,
+                            int64_t k_page_stride, int64_t v_page_stride, const int32_t* page_table,
+                            const int32_t* key_lens, const int32_t* new_lens, int B, int Hq, int Hkv, int Nq, int d,
+                            int n_pages, int page_size, int max_pages, float scale, int causal,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Heads per group of the backward's head-grouped launch order for sequence length N and head
  * dimension d on a device with l2_bytes of L2: a quarter of L2 divided by the bytes of one head's
  * Q, dO and fp32 dQ accumulator (8 * N * d), rounded to nearest and clamped to [1, 16].  Host-only
@@ -191,8 +268,8 @@ FA_API fa_status fa_test_exp2_fma(const float* x, float* y, int n, cudaStream_t 
 
 /* Synchronises `stream`, then reads and clears this device's status word.  Returns
  * FA_ERR_TIMEOUT if a bounded wait ran out in any kernel since the last check,
- * FA_ERR_INTERNAL for other device-detected faults, FA_ERR_CUDA if the synchronisation
- * itself failed, FA_OK otherwise. */
+ * FA_ERR_RANGE if a paged-cache kernel met a value outside the cache, FA_ERR_INTERNAL for other
+ * device-detected faults, FA_ERR_CUDA if the synchronisation itself failed, FA_OK otherwise. */
 FA_API fa_status fa_check(cudaStream_t stream);
 
 /* Description of the last non-OK status returned on the calling thread. */

@@ -23,6 +23,7 @@ finite differences and published hash vectors; none is "parity unpinned".
 """
 from .attention import allowed_mask, forward, backward, forward_rows, backward_head_blocked, forward_decode
 from .dropout import keep_mask, keep_threshold
+from .paged import E4M3, e4m3_encode, e4m3_scale, forward_paged, rotate
 
 __all__ = ["allowed_mask", "forward", "backward", "forward_rows", "backward_head_blocked", "forward_decode",
-           "keep_mask", "keep_threshold"]
+           "keep_mask", "keep_threshold", "E4M3", "e4m3_encode", "e4m3_scale", "forward_paged", "rotate"]
