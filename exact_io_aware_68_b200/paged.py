@@ -12,6 +12,7 @@ Both calls run on the current stream of the pools' device, and can be captured i
 replays read the lengths and the table anew.
 """
 import ctypes
+import functools
 import math
 
 import torch
@@ -26,44 +27,74 @@ def _need(ok, text):
         raise ValueError(text)
 
 
-def _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d):
-    """(e4m3?, device) of the pools, after the checks that both calls share."""
-    dev, dt, shape = k_cache.device, k_cache.dtype, k_cache.shape
+def _cache_fits(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d, dev):
+    """Whether the cache's tensors fit one another: the quick form of ``_refuse_cache``, which says what does not."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != d or v_cache.shape != shape or not k_cache.is_cuda:
+        return False
+    inner = (shape[2] * d, d, 1)
+    dt = k_cache.dtype
+    if dt is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            return False
+        pages = shape[:2]
+        if not (k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32 and k_scale.shape == pages and v_scale.shape == pages
+                and k_scale.is_contiguous() and v_scale.is_contiguous() and k_scale.get_device() == dev == v_scale.get_device()):
+            return False
+    elif dt is not torch.bfloat16 or k_scale is not None or v_scale is not None:
+        return False
+    if new_lens is not None and not (new_lens.dtype is torch.int32 and new_lens.shape == (B,) and new_lens.is_contiguous()
+                                     and new_lens.get_device() == dev):
+        return False
+    return (v_cache.dtype is dt and k_cache.stride()[1:] == inner and v_cache.stride()[1:] == inner and v_cache.get_device() == dev
+            and key_lens.dtype is torch.int32 and key_lens.shape == (B,) and key_lens.is_contiguous() and key_lens.get_device() == dev
+            and page_table.dtype is torch.int32 and page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_contiguous()
+            and page_table.get_device() == dev)
+
+
+def _refuse_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d):
+    """Raises for the first of the cache's tensors that does not fit."""
+    dev, dt, shape = k_cache.device, k_cache.dtype, tuple(k_cache.shape)
     _need(k_cache.is_cuda, "k_cache must be a CUDA tensor")
     fp8 = dt == torch.float8_e4m3fn
     _need(fp8 or dt == torch.bfloat16, f"k_cache must be bfloat16 or float8_e4m3fn, got {dt}")
-    _need(v_cache.dtype == dt, f"v_cache must be {dt} like k_cache, got {v_cache.dtype}")
-    _need(len(shape) == 4 and v_cache.shape == shape, f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be "
+    _need(len(shape) == 4 and tuple(v_cache.shape) == shape, f"k_cache {shape} and v_cache {tuple(v_cache.shape)} must be "
           "[n_pages, Hkv, page_size, d], both the same")
-    n_pages, Hkv, page, dd = shape
-    _need(dd == d, f"the pools have d = {dd}, the heads {d}")
-    inner = (page * d, d, 1)
+    _need(shape[3] == d, f"the pools have d = {shape[3]}, the heads {d}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(t.stride()[1:] == inner, f"{name} must be contiguous within a page")
+        _need(t.stride()[1:] == (shape[2] * d, d, 1), f"{name} must be contiguous within a page")
     _need((k_scale is not None) == fp8 and (v_scale is not None) == fp8, "k_scale and v_scale go with float8_e4m3fn pools")
-    for name, t, dtype, sh in (("v_cache", v_cache, dt, shape), ("k_scale", k_scale, torch.float32, (n_pages, Hkv)),
-                               ("v_scale", v_scale, torch.float32, (n_pages, Hkv)),
-                               ("key_lens", key_lens, torch.int32, (B,)), ("new_lens", new_lens, torch.int32, (B,)),
-                               ("page_table", page_table, torch.int32, None)):
+    for name, t, dtype, sh in (("v_cache", v_cache, dt, shape), ("k_scale", k_scale, torch.float32, shape[:2]),
+                               ("v_scale", v_scale, torch.float32, shape[:2]), ("key_lens", key_lens, torch.int32, (B,)),
+                               ("new_lens", new_lens, torch.int32, (B,)), ("page_table", page_table, torch.int32, None)):
         if t is None:
             continue
         _need(t.device == dev, f"{name} is on {t.device}, k_cache on {dev}")
         _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-        if name != "v_cache":
-            _need(t.is_contiguous(), f"{name} must be contiguous")
-        _need(sh is None or t.shape == sh, f"{name} has shape {tuple(t.shape)}, expected {sh}")
+        _need(name == "v_cache" or t.is_contiguous(), f"{name} must be contiguous")
+        _need(sh is None or tuple(t.shape) == sh, f"{name} has shape {tuple(t.shape)}, expected {sh}")
     _need(page_table.dim() == 2 and page_table.shape[0] == B, f"page_table has shape {tuple(page_table.shape)}, expected "
           f"({B}, max_pages)")
-    return fp8, dev
+    raise ValueError("the tensors of the cache do not fit one another")
+
+
+def _fits(t, dtype, shape, dev):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
 
 
 def _call(dev, name, *args):
-    """The entry point on the current stream of `dev`, with that device current for the call."""
-    if dev.index == torch.cuda.current_device():
-        _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    """The entry point on the current stream of device `dev`, with that device current for the call."""
+    if dev == torch.cuda.current_device():
+        _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+            _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(B, Hq, Hkv, Nq, d, dev):
+    with torch.cuda.device(dev):
+        return _lib.load().fa_fwd_paged_workspace_size(B, Hq, Hkv, Nq, d)
 
 
 def rope_tables(max_pos, rot_dim, base=10000.0, device="cuda"):
@@ -81,56 +112,64 @@ def kv_append(k, v, k_cache, v_cache, page_table, key_lens, new_lens=None, rope=
     contiguous (views of a projection's output need no copy).  rope: (cos, sin) tables, applied to k and q by position
     (``rope_tables``); interleaved: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Writes the pools (and
     the scales of e4m3 pools) in place; returns the rotated queries, contiguous [B, Hq, Nq, d], or None."""
-    _need(k.dim() == 4 and v.shape == k.shape, f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, Hkv, Nq, d], both the same")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, Hkv, Nq, d], both the same")
     B, Hkv, Nq, d = k.shape
-    fp8, dev = _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d)
-    n_pages, heads, page = k_cache.shape[:3]
-    _need(heads == Hkv, f"the pools have {heads} heads, k has {Hkv}")
+    dev = k_cache.get_device()
+    if not _cache_fits(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d, dev):
+        _refuse_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d)
+    n_pages, heads, page, _ = k_cache.shape
+    if heads != Hkv:
+        raise ValueError(f"the pools have {heads} heads, k has {Hkv}")
+    bf16 = torch.bfloat16
     Hq = Hkv
     if q is not None:
-        _need(q.dim() == 4 and q.shape[0] == B and q.shape[2:] == k.shape[2:], f"q has shape {tuple(q.shape)}, expected "
-              f"({B}, Hq, {Nq}, {d})")
-        Hq = q.shape[1]
+        qs = q.shape
+        if len(qs) != 4 or qs[0] != B or qs[2] != Nq or qs[3] != d:
+            raise ValueError(f"q has shape {tuple(qs)}, expected ({B}, Hq, {Nq}, {d})")
+        Hq = qs[1]
     strides = []
-    for name, t in (("q", q), ("k", k), ("v", v)):
+    for t in (q, k, v):
         if t is None:
-            strides += [0, 0, 0]
+            strides += (0, 0, 0)
             continue
-        _need(t.device == dev, f"{name} is on {t.device}, k_cache on {dev}")
-        _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
-        st = t.stride()
-        _need(st[3] == 1, f"{name} must be contiguous in its last dimension")
+        if t.get_device() != dev or t.dtype is not bf16 or t.stride(3) != 1:
+            name = "q" if t is q else "k" if t is k else "v"
+            _need(t.device == k_cache.device, f"{name} is on {t.device}, k_cache on {k_cache.device}")
+            _need(t.dtype is bf16, f"{name} must be torch.bfloat16, got {t.dtype}")
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        b, h, n, _ = t.stride()
         # the stride of a dimension of size one is never taken
-        strides += [s if n > 1 else 0 for s, n in zip(st[:3], t.shape[:3])]
+        strides += (b if B > 1 else 0, h if t.shape[1] > 1 else 0, n if Nq > 1 else 0)
     cos = sin = None
     max_pos = rot = 0
     if rope is not None:
         cos, sin = rope
         for name, t in (("rope cos", cos), ("rope sin", sin)):
-            _need(t.device == dev and t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 2 and t.shape == cos.shape,
-                  f"{name} must be contiguous fp32 [max_pos, rot / 2] on {dev}, cos and sin alike")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        cos, sin = cos.data_ptr(), sin.data_ptr()
+            if t.dim() != 2 or not _fits(t, torch.float32, cos.shape, dev):
+                raise ValueError(f"{name} must be contiguous fp32 [max_pos, rot / 2] on {k_cache.device}, cos and sin alike")
+        max_pos, half = cos.shape
+        rot, cos, sin = 2 * half, cos.data_ptr(), sin.data_ptr()
     if q is None:
         _need(q_out is None, "q_out goes with q")
-    elif q_out is None:
-        q_out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=dev)
+        q_ptr = out_ptr = None
     else:
-        _need(q_out.device == dev and q_out.dtype == torch.bfloat16 and q_out.is_contiguous() and q_out.shape == q.shape,
-              f"q_out must be contiguous bfloat16 {tuple(q.shape)} on {dev}")
-    _call(dev, "fa_kv_append_e4m3" if fp8 else "fa_kv_append", None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          _STRIDES(*strides), None if q is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          *((k_scale.data_ptr(), v_scale.data_ptr()) if fp8 else ()), k_cache.stride(0), v_cache.stride(0),
-          page_table.data_ptr(), key_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), cos, sin, max_pos, rot,
-          int(bool(interleaved)), B, Hq, Hkv, Nq, d, n_pages, page, page_table.shape[1])
+        if q_out is None:
+            q_out = torch.empty((B, Hq, Nq, d), dtype=bf16, device=k_cache.device)
+        elif not _fits(q_out, bf16, q.shape, dev):
+            raise ValueError(f"q_out must be contiguous bfloat16 {tuple(q.shape)} on {k_cache.device}")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    name, scales = ("fa_kv_append", ()) if k_scale is None else ("fa_kv_append_e4m3", (k_scale.data_ptr(), v_scale.data_ptr()))
+    _call(dev, name, q_ptr, k.data_ptr(), v.data_ptr(), _STRIDES(*strides), out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), *scales,
+          k_cache.stride(0), v_cache.stride(0), page_table.data_ptr(), key_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
+          cos, sin, max_pos, rot, int(bool(interleaved)), B, Hq, Hkv, Nq, d, n_pages, page, page_table.shape[1])
     return q_out
 
 
 def paged_workspace(B, Hq, Hkv, Nq, d, device):
     """A workspace tensor for ``attention_paged`` (torch allocations are 256-byte aligned)."""
-    with torch.cuda.device(device):
-        n = _lib.load().fa_fwd_paged_workspace_size(B, Hq, Hkv, Nq, d)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    device = torch.empty(0, device=device).device
+    return torch.empty(_workspace_bytes(B, Hq, Hkv, Nq, d, device.index), dtype=torch.uint8, device=device)
 
 
 def attention_paged(q, k_cache, v_cache, page_table, key_lens, scale=None, causal=False, new_lens=None, k_scale=None,
@@ -140,24 +179,31 @@ def attention_paged(q, k_cache, v_cache, page_table, key_lens, scale=None, causa
 
     q: bf16 [B, Hq, Nq, d] contiguous, Hq a multiple of the pools' Hkv.  Query i of sequence b stands at position
     key_lens[b] - new_lens[b] + i; causal keeps the keys up to it.  Queries i >= new_lens[b] get O = 0, lse = -inf."""
-    _need(q.dim() == 4, f"q has shape {tuple(q.shape)}, expected [B, Hq, Nq, d]")
-    B, Hq, Nq, d = q.shape
-    fp8, dev = _check_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d)
-    for name, t, dtype, shape in (("q", q, torch.bfloat16, q.shape), ("o", o, torch.bfloat16, q.shape),
-                                  ("lse", lse, torch.float32, q.shape[:3])):
-        if t is not None:
-            _need(t.device == dev and t.dtype == dtype and t.is_contiguous() and t.shape == shape,
-                  f"{name} must be contiguous {dtype} {tuple(shape)} on {dev}")
-    n_pages, Hkv, page = k_cache.shape[:3]
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [B, Hq, Nq, d]")
+    B, Hq, Nq, d = shape
+    dev = k_cache.get_device()
+    if not _cache_fits(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d, dev):
+        _refuse_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d)
+    device = k_cache.device
+    if not _fits(q, torch.bfloat16, shape, dev):
+        raise ValueError(f"q must be contiguous bfloat16 on {device}")
+    n_pages, Hkv, page, _ = k_cache.shape
     if workspace is None:
-        workspace = paged_workspace(B, Hq, Hkv, Nq, d, dev)
-    else:
-        _need(workspace.device == dev and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-              f"workspace must be contiguous uint8 on {dev}")
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
-    _call(dev, "fa_fwd_paged_e4m3" if fp8 else "fa_fwd_paged", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          *((k_scale.data_ptr(), v_scale.data_ptr()) if fp8 else ()), o.data_ptr(), lse.data_ptr(), k_cache.stride(0),
+        workspace = torch.empty(_workspace_bytes(B, Hq, Hkv, Nq, d, dev), dtype=torch.uint8, device=device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be contiguous uint8 on {device}")
+    if o is None:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    elif not _fits(o, torch.bfloat16, shape, dev):
+        raise ValueError(f"o must be contiguous bfloat16 {tuple(shape)} on {device}")
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+    elif not _fits(lse, torch.float32, shape[:3], dev):
+        raise ValueError(f"lse must be contiguous float32 {tuple(shape[:3])} on {device}")
+    name, scales = ("fa_fwd_paged", ()) if k_scale is None else ("fa_fwd_paged_e4m3", (k_scale.data_ptr(), v_scale.data_ptr()))
+    _call(dev, name, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *scales, o.data_ptr(), lse.data_ptr(), k_cache.stride(0),
           v_cache.stride(0), page_table.data_ptr(), key_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
           B, Hq, Hkv, Nq, d, n_pages, page, page_table.shape[1], 1.0 / math.sqrt(d) if scale is None else float(scale),
           int(bool(causal)), workspace.data_ptr(), workspace.numel())
