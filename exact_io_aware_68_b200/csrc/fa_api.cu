@@ -450,12 +450,12 @@ int log2_of(int x) {
   return s;
 }
 
-// Rows of one K/V head's row tile: 8 while its rows fit (the MMA's other 8 rows then carry the
-// probabilities' low halves), else 16.
+// Rows of one K/V head's row tile: 8 while its rows fit, else 16.
 int paged_row_tile(int R) { return R <= 8 ? 8 : 16; }
 // The grid of the split kernel: one CTA per SM; with no device a bound for any.
 int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
-size_t paged_slots(int sms) { return size_t(paged_ctas(sms)) * fa::kPagedWarps * 2; }
+constexpr int kPagedMostWarps = 16;
+size_t paged_slots(int sms) { return size_t(paged_ctas(sms)) * kPagedMostWarps * 2; }
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t paged_ws_bytes(int B, int R, int d, int sms) {
   const size_t rows = paged_slots(sms) * paged_row_tile(R);
@@ -480,16 +480,17 @@ fa_status launch_dependent(void (*kernel)(P), dim3 grid, dim3 block, const P& p,
   return launch_status(what);
 }
 
-template <int D, bool FP8, bool R16>
+template <int D, bool FP8, int NG>
 fa_status launch_paged(fa::PagedParams p, int sms, cudaStream_t s) {
-  using Lt = fa::PagedLayout<D, FP8>;
-  constexpr int RT = R16 ? 16 : 8;
+  using Lt = fa::PagedLayout<D, FP8, NG>;
+  constexpr int RT = 8 * NG;
+  static_assert(Lt::WARPS <= kPagedMostWarps && Lt::bytes(fa::kPagedMaxB) <= 232448, "workspace, shared memory");
   const int ctas = paged_ctas(sms);
-  p.n_warps = ctas * fa::kPagedWarps;
+  p.n_warps = ctas * Lt::WARPS;
   p.row_tiles = (p.R + RT - 1) / RT;
-  fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, R16>, Lt::bytes(fa::kPagedMaxB));
+  fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, NG>, Lt::bytes(fa::kPagedMaxB));
   if (st != FA_OK) return st;
-  fa::fa_paged_split_kernel<D, FP8, R16><<<ctas, 32 * fa::kPagedWarps, Lt::bytes(p.B), s>>>(p);
+  fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(p.B), s>>>(p);
   if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
   const long long rows = (long long)p.B * p.Hkv * p.R;
   // A row tile has about n_warps / (B Hkv row_tiles) partials: one warp merges a row up to 8 of them, else a CTA
@@ -560,11 +561,11 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   p.scale_log2 = scale * 1.4426950408889634f;
   const bool wide = paged_row_tile(R) == 16;
   if (d == 64) {
-    if (fp8) return wide ? launch_paged<64, true, true>(p, sms, s) : launch_paged<64, true, false>(p, sms, s);
-    return wide ? launch_paged<64, false, true>(p, sms, s) : launch_paged<64, false, false>(p, sms, s);
+    if (fp8) return wide ? launch_paged<64, true, 2>(p, sms, s) : launch_paged<64, true, 1>(p, sms, s);
+    return wide ? launch_paged<64, false, 2>(p, sms, s) : launch_paged<64, false, 1>(p, sms, s);
   }
-  if (fp8) return wide ? launch_paged<128, true, true>(p, sms, s) : launch_paged<128, true, false>(p, sms, s);
-  return wide ? launch_paged<128, false, true>(p, sms, s) : launch_paged<128, false, false>(p, sms, s);
+  if (fp8) return wide ? launch_paged<128, true, 2>(p, sms, s) : launch_paged<128, true, 1>(p, sms, s);
+  return wide ? launch_paged<128, false, 2>(p, sms, s) : launch_paged<128, false, 1>(p, sms, s);
 }
 
 fa_status run_append(bool fp8, const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,

@@ -11,16 +11,19 @@
 // m* = max m_i, O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.  With e4m3 pages k = c * ks, where
 // ks is constant over a page, so ks multiplies the finished dot product and vs the probability.
 //
-// Bound: HBM.  A key and its value are 4 D bytes (2 D in e4m3) for 4 D flop per row: at most 16
-// flop per byte for 16 rows.  Each SM gets 23 bytes a cycle of the measured copy rate, i.e. a
-// 16-key tile of bf16 at D = 128 every 350 cycles, in which one warp's m16n8k16 MMAs take 64.
-// The MMA shape with 16 rows wastes nothing that is short, and needs no exchange between warps, so
-// every warp works alone: it walks its own contiguous share of all (sequence, head, key tile)s,
-// loads tiles of 4 KB of K and 4 KB of V into a ring of its own (cp.async, 3 deep: 16 KB in flight
-// per warp, 128 KB per SM) and multiplies them out of shared memory.  Shares are equal to one tile whatever
-// the lengths are, nothing depends on the longest sequence, and the workspace (two partials per
-// warp) depends on the device alone.  A row tile that several warps shared is merged by
-// fa_paged_combine_kernel.
+// Bound: HBM.  A key and its value are 4 D bytes (2 D in e4m3) for 4 D flop per row: at most 32
+// flop per byte for 16 rows.  Each SM gets 23 bytes a cycle of the measured copy rate, i.e. 16 keys
+// of bf16 at D = 128 every 350 cycles.  What has to be hidden is latency (copy, ldmatrix, a chain of MMAs,
+// the exponentials), so the design is many independent warps with few registers:
+//  * Both products are transposed, S^T = K Q^T and O^T = V^T P^T (m16n8k16: 16 keys or 16 features by 8
+//    query rows), so that 8 rows fill the MMA; the other way round half of a 16-row tile, of
+//    the accumulators and of the MMAs would be padding.  K comes by ldmatrix, V by ldmatrix.trans, P^T
+//    turns from accumulator into operand by movmatrix.
+//  * Every warp works alone: it walks its own contiguous share of all (sequence, head, key tile)s and
+//    loads its tiles into a ring of its own (cp.async), with no barrier between warps.  Shares are equal to one tile
+//    whatever the lengths are, nothing depends on the longest sequence, and the workspace (two partials per
+//    warp) depends on the device alone.  A row tile that several warps shared is merged by
+//    fa_paged_combine_kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -30,8 +33,6 @@ namespace fa {
 
 enum : int { kStatusRange = 6 };   // a page number, length or position outside the cache
 
-constexpr int kPagedWarps = 8;
-constexpr int kPagedStages = 3;
 constexpr int kPagedMaxB = 4096;   // the prefix of the tile counts sits in shared memory
 constexpr float kPagedRescale = 8.0f;   // the reference max moves only when a tile exceeds it by 2^8
 constexpr float kPagedPScale = 128.0f;  // e4m3: probabilities enter the f16 MMA times 2^7 (at most 2^15)
@@ -94,6 +95,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}\n" : "=r"(r) : "r"(w));
   return r;
 }
+// the transpose of an 8 x 8 matrix of 16-bit elements, one row pair per lane
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -125,14 +132,17 @@ __device__ __forceinline__ int paged_new_len(const PagedParams& p, int b) {
 // row tile exists.
 __device__ __forceinline__ int paged_sharers(long long W, int n_warps) { return int(W < n_warps ? W : n_warps); }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NG>
 struct PagedLayout {
   static constexpr int ROWB = FP8 ? D : 2 * D;         // bytes of one key
-  static constexpr int KT = 4096 / ROWB;               // keys per tile: 16, 32 or 64
+  static constexpr int TILE = 4096;                    // bytes of a tile's K, and of its V
+  static constexpr int KT = TILE / ROWB;               // keys per tile: 16, 32 or 64
   static constexpr int GROUPS = KT / 16;               // 16-key groups: each inside one page
   static constexpr int CPR = ROWB / 16;                // 16-byte chunks per key
-  static constexpr int STAGE = 2 * 4096 + (FP8 ? 128 : 0);   // K, V, and the groups' scales
-  static constexpr int RING = kPagedWarps * kPagedStages * STAGE;
+  static constexpr int WARPS = NG == 1 ? 12 : 8;
+  static constexpr int STAGES = NG == 1 ? 2 : 3;
+  static constexpr int STAGE = 2 * TILE + (FP8 ? 128 : 0);   // K, V, and the groups' scales
+  static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int bytes(int B) { return RING + (B + 1) * 4; }
   // Byte offset of chunk c of row r, XOR-swizzled so that the 8 rows of an ldmatrix at one chunk
   // fall into different banks.
@@ -148,10 +158,10 @@ struct PagedPos {
   int T, L;       // key tiles and keys of sequence b
 };
 
-template <int D, bool FP8, bool R16>
-__global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(const PagedParams p) {
-  using Lt = PagedLayout<D, FP8>;
-  constexpr int KT = Lt::KT, G = Lt::GROUPS, NT = KT / 8, RT = R16 ? 16 : 8;
+template <int D, bool FP8, int NG>
+__global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_paged_split_kernel(const PagedParams p) {
+  using Lt = PagedLayout<D, FP8, NG>;
+  constexpr int KT = Lt::KT, G = Lt::GROUPS, RT = 8 * NG, WARPS = Lt::WARPS, STAGES = Lt::STAGES, C = D / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
   int* off = reinterpret_cast<int*>(smem + Lt::RING);   // [B + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,8 +169,8 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
 
   // ---- prefix of the sequences' key tiles: every thread sums a run of sequences, then the runs are scanned
   {
-    __shared__ int runs[32 * kPagedWarps];
-    const int per = (p.B + 32 * kPagedWarps - 1) / (32 * kPagedWarps);
+    __shared__ int runs[WARPS];
+    const int per = (p.B + 32 * WARPS - 1) / (32 * WARPS);
     int sum = 0;
     for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
       const int T = paged_new_len(p, b) > 0 ? (paged_key_len(p, b) + KT - 1) / KT : 0;
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
     if (tid == 0) off[0] = 0;
     __syncthreads();
     if (blockIdx.x == 0)
-      for (int b = tid; b <= p.B; b += 32 * kPagedWarps) p.plan[b] = off[b];
+      for (int b = tid; b <= p.B; b += 32 * WARPS) p.plan[b] = off[b];
   }
 
   const int HR = p.Hkv * p.row_tiles;
@@ -220,14 +230,14 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
     }
   };
 
-  const uint32_t ring = smem_u32(smem) + warp * kPagedStages * Lt::STAGE;
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * Lt::STAGE;
   const int page_mask = (1 << p.page_shift) - 1;
   int ids[G];   // pages of the groups of the tile that is loaded next
   auto look_up = [&]() {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int key = ld.t * KT + 16 * g;
-      ids[g] = key < ld.L ? __ldg(p.page_table + (int64_t)ld.b * p.max_pages + (key >> p.page_shift)) : 0;
+    for (int x = 0; x < G; ++x) {
+      const int key = ld.t * KT + 16 * x;
+      ids[x] = key < ld.L ? __ldg(p.page_table + (int64_t)ld.b * p.max_pages + (key >> p.page_shift)) : 0;
     }
   };
   auto load = [&](int stage) {
@@ -236,23 +246,25 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
     constexpr int RPI = 32 / Lt::CPR;   // keys per warp-wide copy
     const int c = lane % Lt::CPR, r0 = lane / Lt::CPR;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int key = ld.t * KT + 16 * g;
-      const bool ok = unsigned(ids[g]) < unsigned(p.n_pages);
+    for (int x = 0; x < G; ++x) {
+      const int key = ld.t * KT + 16 * x;
+      const bool ok = unsigned(ids[x]) < unsigned(p.n_pages);
       if (!ok) record_status(kStatusRange);
-      const int64_t page = ok ? ids[g] : 0;
+      const int64_t page = ok ? ids[x] : 0;
       const int64_t in = ((int64_t)h << p.page_shift) + (key & page_mask);
       const uint8_t* ks = p.k + page * p.k_page_bytes + (in + r0) * Lt::ROWB + c * 16;
       const uint8_t* vs = p.v + page * p.v_page_bytes + (in + r0) * Lt::ROWB + c * 16;
       const int left = ok ? ld.L - key - r0 : 0;
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
-        const int at = Lt::at(16 * g + i * RPI + r0, c);
+        const int at = Lt::at(16 * x + i * RPI + r0, c);
         cp_async16(dst + at, ks + i * RPI * Lt::ROWB, i * RPI < left);
-        cp_async16(dst + 4096 + at, vs + i * RPI * Lt::ROWB, i * RPI < left);
+        cp_async16(dst + Lt::TILE + at, vs + i * RPI * Lt::ROWB, i * RPI < left);
       }
       if constexpr (FP8) {
-        if (lane < 2) cp_async4(dst + 8192 + 8 * g + 4 * lane, (lane == 0 ? p.k_scale : p.v_scale) + page * p.Hkv + h, ok && key < ld.L);
+        if (lane < 2)
+          cp_async4(dst + 2 * Lt::TILE + 8 * x + 4 * lane, (lane == 0 ? p.k_scale : p.v_scale) + page * p.Hkv + h,
+                    ok && key < ld.L);
       }
     }
   };
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
   long long at_load = w0;
   look_up();
 #pragma unroll
-  for (int s = 0; s < kPagedStages - 1; ++s) {
+  for (int s = 0; s < STAGES - 1; ++s) {
     if (at_load < w1) {
       load(s);
       advance(ld);
@@ -269,15 +281,17 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
     cp_async_commit();
   }
 
+  // Fragments: lane = 4 g + t4.  As operand column a lane holds query row g of each group of 8, as
+  // accumulator columns the rows 2 t4 and 2 t4 + 1; accumulator rows are keys (or features) g and g + 8.
   const int g = lane >> 2, t4 = lane & 3;
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m[2], l[2], sc[2];   // rows g and g + 8; sc: score scale in the log2 domain
-  int lim[2], lim_lo;        // keys < lim allowed; lim_lo: the smallest that is not zero
-  float vref = 0.f;          // e4m3: the largest value scale so far, O is in units of it
+  uint32_t qf[NG][C][2];
+  float o[NG][C][4];
+  float m[NG][2], l[NG][2], sc[NG][2];   // rows 2 t4 + i; sc: score scale in the log2 domain
+  int lim[NG][2], limg[NG], lim_lo;      // keys < lim allowed; limg: of row g; lim_lo: the smallest that is not zero
+  float vref = 0.f;                      // e4m3: the largest value scale so far, O is in units of it
   int stage = 0;
   bool fresh = true;
-  long long seg = w0;        // first tile of the running segment
+  long long seg = w0;                    // first tile of the running segment
   for (long long w = w0; w < w1; ++w) {
     if (fresh) {
       // ---- queries and limits of this row tile
@@ -288,22 +302,19 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
       const __nv_bfloat16* qb = p.q + ((int64_t)(cp.b * p.Hkv + h) * p.R + rt * RT) * D;
       lim_lo = cp.L;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = rt * RT + g + 8 * i, qi = row % p.Nq;
-        const bool real = (R16 || i == 0) && row < p.R;
-        lim[i] = real && qi < n ? (p.causal ? max(min(cp.L, cp.L - n + qi + 1), 0) : cp.L) : 0;
-        if (lim[i] > 0) lim_lo = min(lim_lo, lim[i]);   // a row without keys is dropped at the end instead
-        sc[i] = p.scale_log2;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        const uint2* src = reinterpret_cast<const uint2*>(qb + (int64_t)(g + 8 * i) * D);
-        const uint32_t* src1 = reinterpret_cast<const uint32_t*>(src);
+      for (int ng = 0; ng < NG; ++ng) {
+        const int row = rt * RT + 8 * ng + g, qi = row % p.Nq;
+        const bool real = row < p.R;
+        limg[ng] = real && qi < n ? (p.causal ? max(min(cp.L, cp.L - n + qi + 1), 0) : cp.L) : 0;
+        if (limg[ng] > 0) lim_lo = min(lim_lo, limg[ng]);   // a row without keys is dropped at the end instead
+        float rs = p.scale_log2;
         if constexpr (FP8) {
           // f16 queries: each row times a power of two that puts its largest element into [2^14, 2^15)
-          uint2 w2[D / 16];
+          const uint2* src = reinterpret_cast<const uint2*>(qb + (int64_t)(8 * ng + g) * D);
+          uint2 w2[C];
           float mx = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
+          for (int c = 0; c < C; ++c) {
             w2[c] = real ? src[c * 4 + t4] : make_uint2(0u, 0u);
             mx = max3f(mx, fabsf(__uint_as_float(w2[c].x << 16)), fabsf(__uint_as_float(w2[c].x & 0xffff0000u)));
             mx = max3f(mx, fabsf(__uint_as_float(w2[c].y << 16)), fabsf(__uint_as_float(w2[c].y & 0xffff0000u)));
@@ -313,33 +324,41 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
           const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
           const bool scaled = mx > 0.f && mx < INFINITY;
           const float up = scaled ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;    // 2^(14 - e)
-          sc[i] *= scaled ? __uint_as_float(uint32_t(127 - 14 + e) << 23) : 1.f;
+          rs *= scaled ? __uint_as_float(uint32_t(127 - 14 + e) << 23) : 1.f;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            qf[c][i] = pack_f16x2(__uint_as_float(w2[c].x << 16) * up, __uint_as_float(w2[c].x & 0xffff0000u) * up);
-            qf[c][2 + i] = pack_f16x2(__uint_as_float(w2[c].y << 16) * up, __uint_as_float(w2[c].y & 0xffff0000u) * up);
+          for (int c = 0; c < C; ++c) {
+            qf[ng][c][0] = pack_f16x2(__uint_as_float(w2[c].x << 16) * up, __uint_as_float(w2[c].x & 0xffff0000u) * up);
+            qf[ng][c][1] = pack_f16x2(__uint_as_float(w2[c].y << 16) * up, __uint_as_float(w2[c].y & 0xffff0000u) * up);
           }
         } else {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(qb + (int64_t)(8 * ng + g) * D);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            qf[c][i] = real ? src1[c * 8 + t4] : 0u;
-            qf[c][2 + i] = real ? src1[c * 8 + 4 + t4] : 0u;
+          for (int c = 0; c < C; ++c) {
+            qf[ng][c][0] = real ? src[c * 8 + t4] : 0u;
+            qf[ng][c][1] = real ? src[c * 8 + 4 + t4] : 0u;
           }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lim[ng][i] = __shfl_sync(0xffffffffu, limg[ng], 4 * (2 * t4 + i));
+          sc[ng][i] = FP8 ? __shfl_sync(0xffffffffu, rs, 4 * (2 * t4 + i)) : rs;
+          m[ng][i] = -INFINITY;
+          l[ng][i] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[ng][c][e] = 0.f;
       }
       lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
       vref = 6.0185311e-36f;   // 2^-117
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
     }
 
     // ---- the next tile of the list goes into the stage that the previous iteration emptied
-    cp_async_wait<kPagedStages - 2>();
+    cp_async_wait<STAGES - 2>();
     __syncwarp();
     {
-      const int into = stage == 0 ? kPagedStages - 1 : stage - 1;
+      const int into = stage == 0 ? STAGES - 1 : stage - 1;
       if (at_load < w1) {
         load(into);
         advance(ld);
@@ -347,77 +366,86 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
       }
       cp_async_commit();
     }
-    const uint32_t kt = ring + stage * Lt::STAGE, vt = kt + 4096;
+    const uint32_t kt = ring + stage * Lt::STAGE, vt = kt + Lt::TILE;
+    const int k0 = cp.t * KT;
 
-    // ---- S = Q K^T
-    float s[NT][4];
+    // ---- S^T = K Q^T: per 16 keys, two chains of MMAs over the features
+    float s[G][NG][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int x = 0; x < G; ++x) {
+      float s2[NG][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-    const int lrow = (lane & 7) + ((lane >> 4) << 3), lchunk = (lane >> 3) & 1;
+      for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      if constexpr (FP8) {
+        for (int e = 0; e < 4; ++e) s[x][ng][e] = s2[ng][e] = 0.f;
+      constexpr int BATCH = FP8 ? 4 : 8;   // chunk pairs loaded ahead of their MMAs
 #pragma unroll
-        for (int c = 0; c < D / 16; c += 2) {   // two chunks of 16 features
-          uint32_t r[4];
-          ldsm4(r, kt + Lt::at(8 * j + lrow, c + lchunk));
+      for (int c0 = 0; c0 < Lt::CPR; c0 += BATCH) {
+        uint32_t r[BATCH / 2][4];   // keys 0-7 and 8-15 at chunk c, keys 0-7 and 8-15 at chunk c + 1
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int cc = c + (x & 1);
-            mma16816<true>(s[j + (x >> 1)], qf[cc][0], qf[cc][1], qf[cc][2], qf[cc][3], e4m3x2_to_f16x2(r[x]),
-                           e4m3x2_to_f16x2(r[x] >> 16));
+        for (int y = 0; y < BATCH / 2; ++y)
+          ldsm4(r[y], kt + Lt::at(16 * x + (lane & 15), c0 + 2 * y + (lane >> 4)));
+#pragma unroll
+        for (int y = 0; y < BATCH / 2; ++y) {
+          if constexpr (FP8) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t a0 = e4m3x2_to_f16x2(r[y][2 * z]), a2 = e4m3x2_to_f16x2(r[y][2 * z] >> 16);
+              const uint32_t a1 = e4m3x2_to_f16x2(r[y][2 * z + 1]), a3 = e4m3x2_to_f16x2(r[y][2 * z + 1] >> 16);
+#pragma unroll
+              for (int ng = 0; ng < NG; ++ng)
+                mma16816<true>(z == 0 ? s[x][ng] : s2[ng], a0, a1, a2, a3, qf[ng][c0 + 2 * y + z][0], qf[ng][c0 + 2 * y + z][1]);
+            }
+          } else {
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+              mma16816<false>((y & 1) == 0 ? s[x][ng] : s2[ng], r[y][0], r[y][1], r[y][2], r[y][3], qf[ng][c0 / 2 + y][0],
+                              qf[ng][c0 / 2 + y][1]);
           }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t r[4];
-          ldsm4(r, kt + Lt::at(8 * j + lrow, 2 * c + lchunk));
-          mma16816<false>(s[j], qf[c][0], qf[c][1], qf[c][2], qf[c][3], r[0], r[1]);
-          mma16816<false>(s[j + 1], qf[c][0], qf[c][1], qf[c][2], qf[c][3], r[2], r[3]);
-        }
       }
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][ng][e] += s2[ng][e];
     }
     float vsc[G];
     if constexpr (FP8) {
-      float ks[G];
 #pragma unroll
-      for (int x = 0; x < G; ++x)
-        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(ks[x]), "=f"(vsc[x]) : "r"(kt + 8192 + 8 * x));
+      for (int x = 0; x < G; ++x) {
+        float ks;
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(ks), "=f"(vsc[x]) : "r"(kt + 2 * Lt::TILE + 8 * x));
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+        for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-        for (int e = 0; e < (R16 ? 4 : 2); ++e) s[j][e] *= ks[j >> 1];
+          for (int e = 0; e < 4; ++e) s[x][ng][e] *= ks;
+      }
     }
-    const int k0 = cp.t * KT;
     if (k0 + KT > lim_lo) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int x = 0; x < G; ++x)
 #pragma unroll
-        for (int e = 0; e < (R16 ? 4 : 2); ++e)
-          if (k0 + 8 * j + 2 * t4 + (e & 1) >= lim[e >> 1]) s[j][e] = -INFINITY;
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k0 + 16 * x + g + 8 * (e >> 1) >= lim[ng][e & 1]) s[x][ng][e] = -INFINITY;
     }
 
-    // ---- online softmax: o is rescaled by alpha (and, e4m3, by the value scale's move), l by alpha
-    float alpha[2] = {1.f, 1.f}, neg[2] = {0.f, 0.f}, vmove = 1.f;
-    bool moved = false;
+    // ---- online softmax.  The reference max of a row moves only when a score passes it by 2^8; whether any
+    // does is one vote, and only then the rows' maxima are formed across the lanes.  o is rescaled by alpha
+    // (and, e4m3, by the value scale's move), l by alpha.
+    float alpha[NG][2], vmove = 1.f;
+    bool over = false;
 #pragma unroll
-    for (int i = 0; i < (R16 ? 2 : 1); ++i) {
-      float mx = s[0][2 * i];
+    for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) mx = max3f(mx, s[j][2 * i], s[j][2 * i + 1]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      mx *= sc[i];
-      if (mx > m[i] + kPagedRescale) {
-        alpha[i] = ex2_approx(m[i] - mx);
-        m[i] = mx;
-        moved = true;
+      for (int i = 0; i < 2; ++i) {
+        float mx = s[0][ng][i];
+#pragma unroll
+        for (int x = 0; x < G; ++x) mx = max3f(mx, s[x][ng][i], s[x][ng][2 + i]);
+        alpha[ng][i] = mx * sc[ng][i];   // the lane's own maximum, for now
+        over |= alpha[ng][i] > m[ng][i] + kPagedRescale;
       }
-      neg[i] = m[i] == -INFINITY ? 0.f : -m[i];
-    }
     if constexpr (FP8) {
       float vmax = vref;
 #pragma unroll
@@ -425,53 +453,67 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
       if (vmax > vref) {   // the same in every lane
         vmove = vref / vmax;
         vref = vmax;
-        moved = true;
+        over = true;
       }
       const float unit = kPagedPScale / vref;
 #pragma unroll
       for (int x = 0; x < G; ++x) vsc[x] *= unit;
     }
-    if (__any_sync(0xffffffffu, moved)) {
-      const float a0 = alpha[0] * vmove, a1 = alpha[R16 ? 1 : 0] * vmove;
-      l[0] *= alpha[0];
-      l[1] *= alpha[1];
+    if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        o[c][0] *= a0;
-        o[c][1] *= a0;
-        o[c][2] *= a1;
-        o[c][3] *= a1;
+      for (int ng = 0; ng < NG; ++ng) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = alpha[ng][i];
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+          alpha[ng][i] = 1.f;
+          if (mx > m[ng][i] + kPagedRescale) {
+            alpha[ng][i] = ex2_approx(m[ng][i] - mx);
+            m[ng][i] = mx;
+          }
+          l[ng][i] *= alpha[ng][i];
+          alpha[ng][i] *= vmove;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[ng][c][e] *= alpha[ng][e & 1];
       }
     }
-    uint32_t pf[G][4];
+    // P^T as operand columns; 16-bit parts: f16 (e4m3, times the page's value scale), else bf16 in two parts
+    // for up to 8 rows: the product is not what bounds the kernel, and P then has 16 bits
+    constexpr bool LOW = !FP8 && NG == 1;
+    uint32_t pf[G][NG][2], pl[LOW ? G : 1][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int ng = 0; ng < NG; ++ng) {
+      const float n0 = m[ng][0] == -INFINITY ? 0.f : -m[ng][0], n1 = m[ng][1] == -INFINITY ? 0.f : -m[ng][1];
 #pragma unroll
-      for (int i = 0; i < (R16 ? 2 : 1); ++i) {
-        float p0 = ex2_approx(fmaf(s[j][2 * i], sc[i], neg[i])), p1 = ex2_approx(fmaf(s[j][2 * i + 1], sc[i], neg[i]));
-        l[i] += p0 + p1;
-        if constexpr (FP8) {
-          pf[j >> 1][2 * (j & 1) + i] = pack_f16x2(p0 * vsc[j >> 1], p1 * vsc[j >> 1]);
-        } else {
-          const uint32_t hi = pack_bf16x2(p0, p1);
-          pf[j >> 1][2 * (j & 1) + i] = hi;
-          // 8 rows: the MMA's other 8 rows take what rounding P to bf16 leaves, so that P has 16 bits
-          if constexpr (!R16)
-            pf[j >> 1][2 * (j & 1) + 1] =
-                pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+      for (int x = 0; x < G; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float p0 = ex2_approx(fmaf(s[x][ng][2 * y], sc[ng][0], n0)), p1 = ex2_approx(fmaf(s[x][ng][2 * y + 1], sc[ng][1], n1));
+          l[ng][0] += p0;
+          l[ng][1] += p1;
+          if constexpr (FP8) {
+            pf[x][ng][y] = movmatrix_trans(pack_f16x2(p0 * vsc[x], p1 * vsc[x]));
+          } else {
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            pf[x][ng][y] = movmatrix_trans(hi);
+            if constexpr (LOW)
+              pl[x][y] = movmatrix_trans(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
+          }
         }
-      }
-      if constexpr (FP8 && !R16) pf[j >> 1][2 * (j & 1) + 1] = 0u;
     }
 
-    // ---- O += P V.  A value that is not finite must not reach a row that does not see its key (0 * inf):
+    // ---- O^T += V^T P^T.  A value that is not finite must not reach a row that does not see its key (0 * inf):
     // where rows see different keys of the tile and such a value is there, it is taken out of the
     // product and its effect is added to the rows that do see it.
     bool careful = false;
     if (lim_lo < min(cp.L, k0 + KT)) {
       uint32_t bad = 0;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < Lt::TILE / 512; ++x) {
         uint32_t q4[4];
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(q4[0]), "=r"(q4[1]), "=r"(q4[2]), "=r"(q4[3])
                      : "r"(vt + 16 * (32 * x + lane)));
@@ -480,67 +522,96 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
       }
       careful = __any_sync(0xffffffffu, bad != 0);
     }
-    const int vrow = lane & 15, vchunk = lane >> 4;
+    const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
+    // operand rows: the 16 features of a block, in order (bf16) or the even then the odd ones (e4m3)
+    auto values = [&](const uint32_t (&r)[4], int z, uint32_t (&a)[4]) {
+      if constexpr (FP8) {   // r[z], r[2 + z]: keys 0-7 and 8-15 of chunk z
+        a[0] = e4m3x2_to_f16x2(__byte_perm(r[z], 0, 0x4420));
+        a[1] = e4m3x2_to_f16x2(__byte_perm(r[z], 0, 0x4431));
+        a[2] = e4m3x2_to_f16x2(__byte_perm(r[2 + z], 0, 0x4420));
+        a[3] = e4m3x2_to_f16x2(__byte_perm(r[2 + z], 0, 0x4431));
+      } else {               // keys 0-7 at chunks 0 and 1, keys 8-15 at chunks 0 and 1
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = r[e];
+      }
+    };
+    constexpr int PER = FP8 ? 2 : 1;   // feature blocks per ldmatrix
     if (!careful) {
 #pragma unroll
-      for (int x = 0; x < G; ++x)
-#pragma unroll
-        for (int c = 0; c < Lt::CPR; c += 2) {
-          uint32_t r[4];
-          ldsm4_trans(r, vt + Lt::at(16 * x + vrow, c + vchunk));
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if constexpr (FP8) {
-              mma16816<true>(o[2 * (c + y)], pf[x][0], pf[x][1], pf[x][2], pf[x][3],
-                             e4m3x2_to_f16x2(__byte_perm(r[2 * y], 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(r[2 * y + 1], 0, 0x4420)));
-              mma16816<true>(o[2 * (c + y) + 1], pf[x][0], pf[x][1], pf[x][2], pf[x][3],
-                             e4m3x2_to_f16x2(__byte_perm(r[2 * y], 0, 0x4431)), e4m3x2_to_f16x2(__byte_perm(r[2 * y + 1], 0, 0x4431)));
-            } else {
-              mma16816<false>(o[c + y], pf[x][0], pf[x][1], pf[x][2], pf[x][3], r[2 * y], r[2 * y + 1]);
-            }
-          }
-        }
-    } else {
-      // a = 1 where the row sees the key; 16-bit one in the operands' type
-      constexpr uint32_t kOne = FP8 ? 0x3c00u : 0x3f80u;
-#pragma unroll
       for (int x = 0; x < G; ++x) {
-        uint32_t see[4];
+        constexpr int BATCH = C / PER < 4 ? C / PER : 4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = k0 + 16 * x + 8 * (e >> 1) + 2 * t4;
-          see[e] = (R16 || (e & 1) == 0) ? (key < lim[e & 1] ? kOne : 0u) | (key + 1 < lim[e & 1] ? kOne << 16 : 0u) : 0u;
+        for (int c0 = 0; c0 < C / PER; c0 += BATCH) {
+          uint32_t r[BATCH][4];
+#pragma unroll
+          for (int y = 0; y < BATCH; ++y) ldsm4_trans(r[y], vt + Lt::at(16 * x + vrow, 2 * (c0 + y) + vchunk));
+#pragma unroll
+          for (int y = 0; y < BATCH; ++y)
+#pragma unroll
+            for (int z = 0; z < PER; ++z) {
+              uint32_t a[4];
+              values(r[y], z, a);
+              const int c = PER * (c0 + y) + z;
+#pragma unroll
+              for (int ng = 0; ng < NG; ++ng) mma16816<FP8>(o[ng][c], a[0], a[1], a[2], a[3], pf[x][ng][0], pf[x][ng][1]);
+              if constexpr (LOW) mma16816<false>(o[0][c], a[0], a[1], a[2], a[3], pl[x][0], pl[x][1]);
+            }
         }
+      }
+    } else {
+      constexpr uint32_t kOne = FP8 ? 0x3c00u : 0x3f80u, kExp = FP8 ? 0x7c00u : 0x7f80u;   // 1, and the exponent's bits
+#pragma unroll 1
+      for (int x = 0; x < G; ++x) {
+        uint32_t see[NG][2], px[NG][2], plx[2] = {0u, 0u};   // see: 1 where row g sees the key
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t r[4];
-          ldsm4_trans(r, vt + Lt::at(16 * x + vrow, FP8 ? (c >> 1) : c));   // its two upper matrices repeat the lower: vrow < 16
-          uint32_t b[2], up[2], dn[2];
+        for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t w = FP8 ? e4m3x2_to_f16x2(__byte_perm(r[y], 0, (c & 1) ? 0x4431 : 0x4420)) : r[y];
-            constexpr uint32_t kExp = FP8 ? 0x7c00u : 0x7f80u;
-            uint32_t u = 0, d = 0, keep = 0;
+            const int key = k0 + 16 * x + 8 * y + 2 * t4;
+            see[ng][y] = (key < limg[ng] ? kOne : 0u) | (key + 1 < limg[ng] ? kOne << 16 : 0u);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t a = (w >> (16 * z)) & 0xffffu;
-              const bool inf_or_nan = (a & kExp) == kExp, nan = inf_or_nan && (a & ~kExp & 0x7fffu) != 0;
-              if (!inf_or_nan) keep |= 0xffffu << (16 * z);
-              if (nan || (inf_or_nan && !(a & 0x8000u))) u |= kOne << (16 * z);
-              if (nan || (inf_or_nan && (a & 0x8000u))) d |= kOne << (16 * z);
-            }
-            b[y] = w & keep;
-            up[y] = u;
-            dn[y] = d;
+            for (int z = 0; z < G; ++z)
+              if (z == x) {
+                px[ng][y] = pf[z][ng][y];
+                if constexpr (LOW) plx[y] = pl[z][y];
+              }
           }
-          float cu[4] = {0.f, 0.f, 0.f, 0.f}, cd[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<FP8>(o[c], pf[x][0], pf[x][1], pf[x][2], pf[x][3], b[0], b[1]);
-          mma16816<FP8>(cu, see[0], see[1], see[2], see[3], up[0], up[1]);
-          mma16816<FP8>(cd, see[0], see[1], see[2], see[3], dn[0], dn[1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (cu[e] > 0.f) o[c][e] += INFINITY;
-            if (cd[e] > 0.f) o[c][e] -= INFINITY;
+        for (int cc = 0; cc < C / PER; ++cc) {
+          uint32_t r[4];
+          ldsm4_trans(r, vt + Lt::at(16 * x + vrow, 2 * cc + vchunk));
+#pragma unroll
+          for (int z = 0; z < PER; ++z) {
+            uint32_t a[4], up[4], dn[4];
+            values(r, z, a);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t keep = 0;
+              up[e] = dn[e] = 0;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t v = (a[e] >> (16 * q)) & 0xffffu;
+                const bool special = (v & kExp) == kExp, nan = special && (v & ~kExp & 0x7fffu) != 0;
+                if (!special) keep |= 0xffffu << (16 * q);
+                if (nan || (special && !(v & 0x8000u))) up[e] |= kOne << (16 * q);
+                if (nan || (special && (v & 0x8000u))) dn[e] |= kOne << (16 * q);
+              }
+              a[e] &= keep;
+            }
+            const int c = PER * cc + z;
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+              float cu[4] = {0.f, 0.f, 0.f, 0.f}, cd[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<FP8>(o[ng][c], a[0], a[1], a[2], a[3], px[ng][0], px[ng][1]);
+              if constexpr (LOW) mma16816<false>(o[0][c], a[0], a[1], a[2], a[3], plx[0], plx[1]);
+              mma16816<FP8>(cu, up[0], up[1], up[2], up[3], see[ng][0], see[ng][1]);
+              mma16816<FP8>(cd, dn[0], dn[1], dn[2], dn[3], see[ng][0], see[ng][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (cu[e] > 0.f) o[ng][c][e] += INFINITY;
+                if (cd[e] > 0.f) o[ng][c][e] -= INFINITY;
+              }
+            }
           }
         }
       }
@@ -552,54 +623,50 @@ __global__ void __launch_bounds__(32 * kPagedWarps, 1) fa_paged_split_kernel(con
       const bool whole = cp.t + 1 == cp.T && w - seg + 1 == cp.T;
       const int h = cp.hr / p.row_tiles, rt = cp.hr % p.row_tiles;
 #pragma unroll
-      for (int i = 0; i < (R16 ? 2 : 1); ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        const int row = g + 8 * i;
-        if (rt * RT + row >= p.R) continue;
-        const bool dead = lim[i] == 0;
-        if (dead) l[i] = 0.f;
-        const float f = (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? (l[i] != 0.f ? 1.f / l[i] : 0.f) : 1.f);
-        const int64_t out = (int64_t)(cp.b * p.Hkv + h) * p.R + rt * RT + row;
-        const int64_t slot = (2 * (int64_t)me + (seg == w0 ? 0 : 1)) * RT + row;
-        // fragment columns -> features: bf16 pairs 8c + 2 t4; e4m3 quads 16c + 4 t4 (even and odd tiles interleaved)
+      for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-        for (int c = 0; c < D / 8; c += 2) {
-          float x[4];   // o[c] pair, o[c + 1] pair
+        for (int i = 0; i < 2; ++i) {
+          float lr = l[ng][i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float val = o[c + (e >> 1)][2 * i + (e & 1)];
-            if constexpr (!R16) val += o[c + (e >> 1)][2 + (e & 1)];
-            x[e] = dead ? 0.f : val * f;
-          }
-          if constexpr (FP8) {
-            const int at = 8 * c + 4 * t4;
-            if (whole)
-              *reinterpret_cast<uint2*>(p.o + out * D + at) = make_uint2(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[1], x[3]));
-            else
-              *reinterpret_cast<float4*>(p.part_o + slot * D + at) = make_float4(x[0], x[2], x[1], x[3]);
-          } else {
+          for (int z = 4; z < 32; z <<= 1) lr += __shfl_xor_sync(0xffffffffu, lr, z);
+          const int row = 8 * ng + 2 * t4 + i;
+          if (rt * RT + row >= p.R) continue;
+          const bool dead = lim[ng][i] == 0;
+          if (dead) lr = 0.f;
+          const float f = (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? (lr != 0.f ? 1.f / lr : 0.f) : 1.f);
+          const int64_t out = (int64_t)(cp.b * p.Hkv + h) * p.R + rt * RT + row;
+          const int64_t slot = (2 * (int64_t)me + (seg == w0 ? 0 : 1)) * RT + row;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int at = 8 * (c + y) + 2 * t4;
+          for (int c = 0; c < C; ++c) {
+            const float a = dead ? 0.f : o[ng][c][i] * f, b = dead ? 0.f : o[ng][c][2 + i] * f;
+            if constexpr (FP8) {
+              const int at = 16 * c + 2 * g;
               if (whole)
-                *reinterpret_cast<uint32_t*>(p.o + out * D + at) = pack_bf16x2(x[2 * y], x[2 * y + 1]);
+                *reinterpret_cast<uint32_t*>(p.o + out * D + at) = pack_bf16x2(a, b);
               else
-                *reinterpret_cast<float2*>(p.part_o + slot * D + at) = make_float2(x[2 * y], x[2 * y + 1]);
+                *reinterpret_cast<float2*>(p.part_o + slot * D + at) = make_float2(a, b);
+            } else {
+              const int at = 16 * c + g;
+              if (whole) {
+                p.o[out * D + at] = __float2bfloat16_rn(a);
+                p.o[out * D + at + 8] = __float2bfloat16_rn(b);
+              } else {
+                p.part_o[slot * D + at] = a;
+                p.part_o[slot * D + at + 8] = b;
+              }
             }
           }
+          if (g == 0) {
+            if (whole)
+              p.lse[out] = lr != 0.f ? (m[ng][i] + lg2_approx(lr)) * kPagedLn2 : -INFINITY;
+            else
+              p.part_ml[slot] = make_float2(m[ng][i], lr);
+          }
         }
-        if (t4 == 0) {
-          if (whole)
-            p.lse[out] = l[i] != 0.f ? (m[i] + lg2_approx(l[i])) * kPagedLn2 : -INFINITY;
-          else
-            p.part_ml[slot] = make_float2(m[i], l[i]);
-        }
-      }
       fresh = true;
     }
     advance(cp);
-    stage = stage == kPagedStages - 1 ? 0 : stage + 1;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
 }
 
