@@ -457,27 +457,40 @@ int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
 constexpr int kPagedMostWarps = 16;
 size_t paged_slots(int sms) { return size_t(paged_ctas(sms)) * kPagedMostWarps * 2; }
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-size_t paged_ws_bytes(int B, int R, int d, int sms) {
-  const size_t rows = paged_slots(sms) * paged_row_tile(R);
-  return up256(rows * d * 4) + up256(rows * 8) + up256(size_t(B + 1) * 4);
+size_t paged_ws_bytes(int B, int Hkv, int R, int d, int sms) {
+  const size_t rows = paged_slots(sms) * paged_row_tile(R), tiles = size_t(B) * Hkv * ((R + 7) / 8);
+  return up256(rows * d * 4) + up256(rows * 8) + up256(size_t(B + 1) * 4) + up256(tiles * 8);
 }
 
 // Launch as a programmatic dependent of the kernel before it on the stream: the kernel may be
 // scheduled early and waits (griddepcontrol.wait) until that grid has completed.
-template <typename P>
-fa_status launch_dependent(void (*kernel)(P), dim3 grid, dim3 block, const P& p, cudaStream_t s, const char* what) {
+template <typename... P>
+fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, const char* what, P... p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p...);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return launch_status(what);
+}
+
+// Warps per row: 8 while that makes at most 4 CTAs per SM (few rows, many partials each), 4 while it
+// makes at most 16, else 1.
+template <int D>
+fa_status launch_paged_combine(const fa::PagedParams& p, int tile_rows, int sms, cudaStream_t s) {
+  const long long rows = (long long)p.B * p.Hkv * p.R;
+  const char* what = "fa_fwd_paged combine kernel launch";
+  if (rows <= 4LL * sms)
+    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 8>, unsigned(rows), 256, s, what, p, tile_rows);
+  if (rows <= 32LL * sms)
+    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 4>, unsigned((rows + 1) / 2), 256, s, what, p, tile_rows);
+  return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 1>, unsigned((rows + 7) / 8), 256, s, what, p, tile_rows);
 }
 
 template <int D, bool FP8, int NG>
@@ -492,13 +505,7 @@ fa_status launch_paged(fa::PagedParams p, int sms, cudaStream_t s) {
   if (st != FA_OK) return st;
   fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(p.B), s>>>(p);
   if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
-  const long long rows = (long long)p.B * p.Hkv * p.R;
-  // A row tile has about n_warps / (B Hkv row_tiles) partials: one warp merges a row up to 8 of them, else a CTA
-  if ((long long)p.n_warps > 8LL * p.B * p.Hkv * p.row_tiles)
-    return launch_dependent(fa::fa_paged_combine_kernel<D, RT, 8>, dim3(unsigned(rows)), dim3(256), p, s,
-                            "fa_fwd_paged combine kernel launch");
-  return launch_dependent(fa::fa_paged_combine_kernel<D, RT, 1>, dim3(unsigned((rows + 7) / 8)), dim3(256), p, s,
-                          "fa_fwd_paged combine kernel launch");
+  return launch_paged_combine<D>(p, RT, sms, s);
 }
 
 fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -527,10 +534,10 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
     return fail(FA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   int sms = 0;
   const int R = Hq / Hkv * Nq;
-  const size_t least = paged_ws_bytes(B, R, d, 1);   // refused without a device too
+  const size_t least = paged_ws_bytes(B, Hkv, R, d, 1);   // refused without a device too
   if (workspace_bytes < least) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs more than %zu", workspace_bytes, least);
   if ((st = sm_count(&sms)) != FA_OK) return st;
-  const size_t need = paged_ws_bytes(B, R, d, sms);
+  const size_t need = paged_ws_bytes(B, Hkv, R, d, sms);
   if (workspace_bytes < need) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
   const size_t rows = paged_slots(sms) * paged_row_tile(R);
   fa::PagedParams p{};
@@ -545,6 +552,7 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + up256(rows * d * 4));
   p.plan = reinterpret_cast<int*>(ws + up256(rows * d * 4) + up256(rows * 8));
+  p.info = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.plan) + up256(size_t(B + 1) * 4));
   p.page_table = page_table;
   p.key_lens = key_lens;
   p.new_lens = new_lens;
@@ -971,7 +979,7 @@ fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void* o, fl
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || d < 1 || B > fa::kPagedMaxB) return 0;
   if (int64_t(B) * Hq * Nq >= (int64_t(1) << 31)) return 0;
-  return paged_ws_bytes(B, Hq / Hkv * Nq, d, decode_sms());
+  return paged_ws_bytes(B, Hkv, Hq / Hkv * Nq, d, decode_sms());
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, int64_t k_page_stride,

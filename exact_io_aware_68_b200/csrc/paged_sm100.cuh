@@ -49,6 +49,7 @@ struct PagedParams {
   float* part_o;               // [2 * warps][row tile][D] fp32, unnormalised
   float2* part_ml;             // [2 * warps][row tile]: m (log2 domain), l
   int* plan;                   // [B + 1]: prefix of the sequences' key tiles
+  int2* info;                  // [B, Hkv, row_tiles]: slot of the first partial; warp of the last, or -1: no partials
   const int32_t* page_table;   // [B, max_pages]
   const int32_t* key_lens;     // [B]
   const int32_t* new_lens;     // [B] or null
@@ -131,6 +132,12 @@ __device__ __forceinline__ int paged_new_len(const PagedParams& p, int b) {
 // How many warps share W tiles: no share is empty, so every partial between the first and the last warp of a
 // row tile exists.
 __device__ __forceinline__ int paged_sharers(long long W, int n_warps) { return int(W < n_warps ? W : n_warps); }
+// First tile of sharer i of n < 2^15: floor(W i / n), by 32-bit divisions where W fits.
+__device__ __forceinline__ long long paged_share(long long W, int i, int n) {
+  if (W >> 32) return W * i / n;
+  const unsigned q = unsigned(W) / unsigned(n), r = unsigned(W) % unsigned(n);
+  return (long long)q * i + r * unsigned(i) / unsigned(n);
+}
 
 template <int D, bool FP8, int NG>
 struct PagedLayout {
@@ -200,11 +207,11 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   const int me = warp * int(gridDim.x) + int(blockIdx.x);
   const int sharers = paged_sharers(W, p.n_warps);
   if (me >= sharers) return;
-  const long long w0 = W * me / sharers, w1 = W * (me + 1) / sharers;
+  const long long w0 = paged_share(W, me, sharers), w1 = paged_share(W, me + 1, sharers);
 
   PagedPos ld;
   {
-    const int want = int(w0 / HR);   // the sequence with off[b] <= want < off[b + 1]
+    const int want = (W >> 32) ? int(w0 / HR) : int(unsigned(w0) / unsigned(HR));   // the sequence with off[b] <= want < off[b + 1]
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -213,8 +220,8 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
     ld.b = lo;
     ld.T = off[lo + 1] - off[lo];
     const long long rem = w0 - (long long)off[lo] * HR;
-    ld.hr = int(rem / ld.T);
-    ld.t = int(rem % ld.T);
+    ld.hr = (rem >> 32) ? int(rem / ld.T) : int(unsigned(rem) / unsigned(ld.T));
+    ld.t = int(rem - (long long)ld.hr * ld.T);
     ld.L = paged_key_len(p, lo);
   }
   PagedPos cp = ld;
@@ -622,6 +629,11 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
     if (cp.t + 1 == cp.T || w + 1 == w1) {
       const bool whole = cp.t + 1 == cp.T && w - seg + 1 == cp.T;
       const int h = cp.hr / p.row_tiles, rt = cp.hr % p.row_tiles;
+      if (lane == 0) {
+        int2* info = p.info + cp.b * HR + cp.hr;
+        if (cp.t + 1 == cp.T) info->y = whole ? -1 : me;
+        if (cp.t - int(w - seg) == 0) info->x = 2 * me + (seg == w0 ? 0 : 1);
+      }
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -670,46 +682,58 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   }
 }
 
-// Merges the partials of one query row that several warps made; one warp (WPR = 1) or one CTA of
-// WPR warps per row.  Rows of a row tile that one warp had whole are done already.  Also writes the rows of
-// sequences without keys or without new tokens: O = 0, lse = -inf.
-template <int D, int RT, int WPR>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p) {
+// Merges the partials of one query row that several warps made, WPR warps of a CTA per row, four partials
+// in flight per warp.  Rows of a row tile that one warp had whole are done already.  Also writes the rows
+// of sequences without keys or without new tokens: O = 0, lse = -inf.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, const int tile_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = WPR == 1 ? (long long)blockIdx.x * 8 + warp : (long long)blockIdx.x;   // of [B, Hkv, R]
-  if (row >= (long long)p.B * p.Hkv * p.R) return;
-  const int r = int(row % p.R), h = int(row / p.R % p.Hkv), b = int(row / p.R / p.Hkv);
-  constexpr int PER = D / 32;
-  const int T = p.plan[b + 1] - p.plan[b], HR = p.Hkv * p.row_tiles;
-  const long long W = (long long)p.plan[p.B] * HR;
+  constexpr int PER = D / 32, RPC = 8 / WPR;   // features per lane, rows per CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const unsigned row = blockIdx.x * RPC + warp / WPR;   // of [B, Hkv, R]; B Hq Nq < 2^31
+  const bool real = row < unsigned(p.B) * p.Hkv * p.R;
+  const unsigned bh = real ? row / p.R : 0, r = row % p.R, b = bh / p.Hkv;
+  const int has = p.plan[b + 1] - p.plan[b];
+  const int2 info = p.info[bh * p.row_tiles + r / tile_rows];
   float acc[PER], ms = -INFINITY, ls = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  if (T > 0) {
-    const long long first = (long long)p.plan[b] * HR + (long long)(h * p.row_tiles + r / RT) * T;
-    const int sharers = paged_sharers(W, p.n_warps);
-    const int w_first = int(((first + 1) * sharers - 1) / W), w_last = int(((first + T) * sharers - 1) / W);
-    if (w_first == w_last) return;
-    const int sub = WPR == 1 ? 0 : warp;
-    for (int w = w_first + sub; w <= w_last; w += WPR) {
-      const long long starts = W * w / sharers;
-      const int64_t slot = (2 * (int64_t)w + (starts >= first ? 0 : 1)) * RT + r % RT;
-      const float2 ml = p.part_ml[slot];
-      float x[PER];
+  auto add = [&](float m, float l, const float* x) {
+    if (l == 0.f) return;   // no key seen there (its m may be -inf)
+    const float mn = fmaxf(ms, m);
+    const float a = ms == -INFINITY ? 0.f : ex2_approx(ms - mn), c = ex2_approx(m - mn);
+    ls = ls * a + l * c;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) x[e] = p.part_o[slot * D + lane * PER + e];
-      if (ml.y == 0.f) continue;   // no key seen there (its m may be -inf)
-      const float mn = fmaxf(ms, ml.x);
-      const float a = ms == -INFINITY ? 0.f : ex2_approx(ms - mn), c = ex2_approx(ml.x - mn);
-      ls = ls * a + ml.y * c;
+    for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + x[e] * c;
+    ms = mn;
+  };
+  const bool whole = has > 0 && info.y < 0;
+  if (real && has > 0 && !whole) {
+    const int first = info.x >> 1;   // the first warp's slot may be its second, the others' is their first
+    for (int w0 = first + sub; w0 <= info.y; w0 += 4 * WPR) {
+      float2 ml[4];
+      float x[4][PER];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + x[e] * c;
-      ms = mn;
+      for (int u = 0; u < 4; ++u) {
+        const int w = w0 + u * WPR;
+        ml[u] = make_float2(0.f, 0.f);
+        if (w > info.y) continue;
+        const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * tile_rows + r % tile_rows;
+        ml[u] = p.part_ml[slot];
+        if constexpr (PER == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(p.part_o + slot * D + lane * 4);
+          x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(p.part_o + slot * D + lane * 2);
+          x[u][0] = f.x; x[u][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(ml[u].x, ml[u].y, x[u]);
     }
   }
   if constexpr (WPR > 1) {
-    __shared__ float sm[WPR], sl[WPR], so[WPR][D];
+    __shared__ float sm[8], sl[8], so[8][D];
     if (lane == 0) {
       sm[warp] = ms;
       sl[warp] = ls;
@@ -717,24 +741,15 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
 #pragma unroll
     for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = acc[e];
     __syncthreads();
-    if (warp != 0) return;
-    for (int x = 1; x < WPR; ++x) {
-      if (sl[x] == 0.f) continue;
-      const float mn = fmaxf(ms, sm[x]);
-      const float a = ms == -INFINITY ? 0.f : ex2_approx(ms - mn), c = ex2_approx(sm[x] - mn);
-      ls = ls * a + sl[x] * c;
+    if (sub != 0) return;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + so[x][lane * PER + e] * c;
-      ms = mn;
-    }
+    for (int y = 1; y < WPR; ++y) add(sm[warp + y], sl[warp + y], &so[warp + y][lane * PER]);
   }
+  if (!real || whole) return;
   const float inv = ls != 0.f ? 1.f / ls : 0.f;
-  uint32_t out[PER / 2];
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)row * D + lane * PER);
 #pragma unroll
-  for (int e = 0; e < PER / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
-#pragma unroll
-  for (int e = 0; e < PER / 2; ++e) dst[e] = out[e];
+  for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   if (lane == 0) p.lse[row] = ls != 0.f ? (ms + lg2_approx(ls)) * kPagedLn2 : -INFINITY;
 }
 
