@@ -21,6 +21,7 @@
 #include "fwd_sm100.cuh"
 #include "kv_append.cuh"
 #include "paged_sm100.cuh"
+#include "paged_wide_sm100.cuh"
 #include "simt_f32.cuh"
 
 namespace {
@@ -450,25 +451,61 @@ int log2_of(int x) {
   return s;
 }
 
-// Rows of one K/V head's row tile: 8 while its rows fit, else 16.
-int paged_row_tile(int R) { return R <= 8 ? 8 : 16; }
-// The grid of the split kernel: one CTA per SM; with no device a bound for any.
+// How fa_fwd_paged cuts its rows, by sizes alone (host arithmetic).  R = (Hq / Hkv) Nq query rows share a K/V head:
+//  * up to 16 rows, or what the wide kernel's plan cannot index: tiles of 8 (R <= 8) or 16 consecutive rows,
+//    independent warps (paged_sm100.cuh);
+//  * more: pairs of 128-row tiles on the tensor memory path (paged_wide_sm100.cuh).
+struct PagedShape {
+  bool wide;
+  int rows;        // of a tile (wide: of a pair: 256)
+  int tq;          // rows, or positions, per tile
+  int tiles;       // tiles (pairs) per (sequence, K/V head)
+  int64_t plan;    // entries of the plan
+};
+PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int64_t max_keys) {
+  const int g = Hq / Hkv, R = g * Nq;
+  PagedShape s{};
+  if (R > 16 && g <= 128) {
+    s.tq = 128 / g;
+    s.tiles = (Nq + 2 * s.tq - 1) / (2 * s.tq);
+    s.rows = 256;
+    s.plan = int64_t(B) * s.tiles + 1;
+    s.wide = s.plan * ((max_keys + 127) / 128) < (int64_t(1) << 31);
+    if (s.wide) return s;
+  }
+  s.wide = false;
+  s.rows = s.tq = R <= 8 ? 8 : 16;
+  s.tiles = (R + s.rows - 1) / s.rows;
+  s.plan = B + 1;
+  return s;
+}
+// The grids of the split and of the wide kernel: one CTA per SM; with no device a bound for any.
 int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
 constexpr int kPagedMostWarps = 16;
-size_t paged_slots(int sms) { return size_t(paged_ctas(sms)) * kPagedMostWarps * 2; }
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-size_t paged_ws_bytes(int B, int Hkv, int R, int d, int sms) {
-  const size_t rows = paged_slots(sms) * paged_row_tile(R), tiles = size_t(B) * Hkv * ((R + 7) / 8);
-  return up256(rows * d * 4) + up256(rows * 8) + up256(size_t(B + 1) * 4) + up256(tiles * 8);
+// The workspace: partial O, partial (m, l), plan, info.
+struct PagedSpace {
+  size_t ml, plan, info, total;   // byte offsets
+};
+PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
+  const size_t rows = size_t(paged_ctas(sms)) * (s.wide ? 1 : kPagedMostWarps) * 2 * s.rows;
+  PagedSpace w;
+  w.ml = up256(rows * d * 4);
+  w.plan = w.ml + up256(rows * 8);
+  w.info = w.plan + up256(size_t(s.plan) * 4);
+  w.total = w.info + up256(size_t(B) * Hkv * s.tiles * 8);
+  return w;
 }
 
 // Launch as a programmatic dependent of the kernel before it on the stream: the kernel may be
 // scheduled early and waits (griddepcontrol.wait) until that grid has completed.
 template <typename... P>
-fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, const char* what, P... p) {
+fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, unsigned smem, cudaStream_t s, const char* what,
+                           P... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -482,30 +519,82 @@ fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, 
 
 // Warps per row: 8 while that makes at most 4 CTAs per SM (few rows, many partials each), 4 while it
 // makes at most 16, else 1.
-template <int D>
-fa_status launch_paged_combine(const fa::PagedParams& p, int tile_rows, int sms, cudaStream_t s) {
-  const long long rows = (long long)p.B * p.Hkv * p.R;
+template <int D, bool WIDE>
+fa_status launch_paged_combine(const fa::WideParams& q, int sms, cudaStream_t s) {
+  const long long rows = (long long)q.p.B * q.p.Hkv * q.p.R;
   const char* what = "fa_fwd_paged combine kernel launch";
   if (rows <= 4LL * sms)
-    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 8>, unsigned(rows), 256, s, what, p, tile_rows);
+    return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 8, WIDE>, unsigned(rows), 256, 0, s, what, q);
   if (rows <= 32LL * sms)
-    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 4>, unsigned((rows + 1) / 2), 256, s, what, p, tile_rows);
-  return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 1>, unsigned((rows + 7) / 8), 256, s, what, p, tile_rows);
+    return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 4, WIDE>, unsigned((rows + 1) / 2), 256, 0, s, what, q);
+  return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 1, WIDE>, unsigned((rows + 7) / 8), 256, 0, s, what, q);
 }
 
 template <int D, bool FP8, int NG>
-fa_status launch_paged(fa::PagedParams p, int sms, cudaStream_t s) {
+fa_status launch_paged(fa::WideParams q, int sms, cudaStream_t s) {
   using Lt = fa::PagedLayout<D, FP8, NG>;
-  constexpr int RT = 8 * NG;
   static_assert(Lt::WARPS <= kPagedMostWarps && Lt::bytes(fa::kPagedMaxB) <= 232448, "workspace, shared memory");
   const int ctas = paged_ctas(sms);
-  p.n_warps = ctas * Lt::WARPS;
-  p.row_tiles = (p.R + RT - 1) / RT;
+  q.p.n_warps = ctas * Lt::WARPS;
   fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, NG>, Lt::bytes(fa::kPagedMaxB));
   if (st != FA_OK) return st;
-  fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(p.B), s>>>(p);
+  fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(q.p.B), s>>>(q.p);
   if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
-  return launch_paged_combine<D>(p, RT, sms, s);
+  return launch_paged_combine<D, false>(q, sms, s);
+}
+
+// Pool of pages as {d, page_size, Hkv, n_pages}, loaded page by page (at most 128 rows): 64 features with the
+// 128-byte swizzle in bf16, whole rows unswizzled in e4m3.
+fa_status make_pool_map(CUtensorMap* map, const void* ptr, bool fp8, int d, int page_size, int Hkv, int n_pages,
+                        int64_t page_bytes, const char* name) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  const cuuint64_t row = cuuint64_t(d) * (fp8 ? 1 : 2);
+  const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(page_size), cuuint64_t(Hkv), cuuint64_t(n_pages)};
+  const cuuint64_t strides[3] = {row, row * page_size, cuuint64_t(page_bytes)};
+  const cuuint32_t box[4] = {cuuint32_t(fp8 ? d : 64), cuuint32_t(page_size < 128 ? page_size : 128), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
+                        dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, int(r));
+  return FA_OK;
+}
+// Queries as {d, heads of a group, Nq, B * Hkv}: a box is 64 features of all the group's heads at tq positions.
+fa_status make_group_map(CUtensorMap* map, const void* ptr, int d, int g, int Nq, int BH, int tq) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  const cuuint64_t row = cuuint64_t(d) * 2;
+  const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(g), cuuint64_t(Nq), cuuint64_t(BH)};
+  const cuuint64_t strides[3] = {row * Nq, row, row * Nq * g};
+  const cuuint32_t box[4] = {64, cuuint32_t(g), cuuint32_t(tq), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed with CUresult %d", int(r));
+  return FA_OK;
+}
+
+template <int D, bool FP8>
+fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cudaStream_t s) {
+  using L = fa::WideLayout<D, FP8>;
+  CUtensorMap mq, mk, mv;
+  fa_status st;
+  const fa::PagedParams& p = q.p;
+  if ((st = make_group_map(&mq, p.q, D, q.g, p.Nq, p.B * p.Hkv, q.tq)) != FA_OK) return st;
+  if ((st = make_pool_map(&mk, p.k, FP8, D, page_size, p.Hkv, p.n_pages, p.k_page_bytes, "k_cache")) != FA_OK) return st;
+  if ((st = make_pool_map(&mv, p.v, FP8, D, page_size, p.Hkv, p.n_pages, p.v_page_bytes, "v_cache")) != FA_OK) return st;
+  auto kernel = fa::fa_paged_wide_kernel<D, FP8>;
+  if ((st = set_smem(kernel, L::BYTES)) != FA_OK) return st;
+  if ((st = check_launch_regs(kernel, L::LAUNCH_REGS, "fa_fwd_paged wide kernel")) != FA_OK) return st;
+  fa::fa_paged_plan_kernel<<<1, 1024, 0, s>>>(q);
+  if ((st = launch_status("fa_fwd_paged plan kernel launch")) != FA_OK) return st;
+  st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
+      kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mk, mv, q);
+  if (st != FA_OK) return st;
+  return launch_paged_combine<D, true>(q, sms, s);
 }
 
 fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -533,14 +622,15 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(FA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   int sms = 0;
-  const int R = Hq / Hkv * Nq;
-  const size_t least = paged_ws_bytes(B, Hkv, R, d, 1);   // refused without a device too
+  const PagedShape shape = paged_shape(B, Hq, Hkv, Nq, int64_t(max_pages) * page_size);
+  const size_t least = paged_space(B, Hkv, shape, d, 1).total;   // refused without a device too
   if (workspace_bytes < least) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs more than %zu", workspace_bytes, least);
   if ((st = sm_count(&sms)) != FA_OK) return st;
-  const size_t need = paged_ws_bytes(B, Hkv, R, d, sms);
-  if (workspace_bytes < need) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-  const size_t rows = paged_slots(sms) * paged_row_tile(R);
-  fa::PagedParams p{};
+  const PagedSpace space = paged_space(B, Hkv, shape, d, sms);
+  if (workspace_bytes < space.total)
+    return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, space.total);
+  fa::WideParams q4{};
+  fa::PagedParams& p = q4.p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const uint8_t*>(k_cache);
   p.v = static_cast<const uint8_t*>(v_cache);
@@ -550,9 +640,9 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + up256(rows * d * 4));
-  p.plan = reinterpret_cast<int*>(ws + up256(rows * d * 4) + up256(rows * 8));
-  p.info = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.plan) + up256(size_t(B + 1) * 4));
+  p.part_ml = reinterpret_cast<float2*>(ws + space.ml);
+  p.plan = reinterpret_cast<int*>(ws + space.plan);
+  p.info = reinterpret_cast<int2*>(ws + space.info);
   p.page_table = page_table;
   p.key_lens = key_lens;
   p.new_lens = new_lens;
@@ -561,19 +651,28 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   p.B = B;
   p.Hkv = Hkv;
   p.Nq = Nq;
-  p.R = R;
+  p.R = Hq / Hkv * Nq;
+  p.row_tiles = shape.tiles;
   p.n_pages = n_pages;
   p.page_shift = log2_of(page_size);
   p.max_pages = max_pages;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const bool wide = paged_row_tile(R) == 16;
-  if (d == 64) {
-    if (fp8) return wide ? launch_paged<64, true, 2>(p, sms, s) : launch_paged<64, true, 1>(p, sms, s);
-    return wide ? launch_paged<64, false, 2>(p, sms, s) : launch_paged<64, false, 1>(p, sms, s);
+  q4.g = Hq / Hkv;
+  q4.tq = shape.tq;
+  q4.n_pairs = shape.tiles;
+  q4.wait_ns = g_wait_ns.load();
+  if (shape.wide) {
+    if (d == 64) return fp8 ? launch_paged_wide<64, true>(q4, page_size, sms, s) : launch_paged_wide<64, false>(q4, page_size, sms, s);
+    return fp8 ? launch_paged_wide<128, true>(q4, page_size, sms, s) : launch_paged_wide<128, false>(q4, page_size, sms, s);
   }
-  if (fp8) return wide ? launch_paged<128, true, 2>(p, sms, s) : launch_paged<128, true, 1>(p, sms, s);
-  return wide ? launch_paged<128, false, 2>(p, sms, s) : launch_paged<128, false, 1>(p, sms, s);
+  const bool two = shape.rows == 16;
+  if (d == 64) {
+    if (fp8) return two ? launch_paged<64, true, 2>(q4, sms, s) : launch_paged<64, true, 1>(q4, sms, s);
+    return two ? launch_paged<64, false, 2>(q4, sms, s) : launch_paged<64, false, 1>(q4, sms, s);
+  }
+  if (fp8) return two ? launch_paged<128, true, 2>(q4, sms, s) : launch_paged<128, true, 1>(q4, sms, s);
+  return two ? launch_paged<128, false, 2>(q4, sms, s) : launch_paged<128, false, 1>(q4, sms, s);
 }
 
 fa_status run_append(bool fp8, const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
@@ -979,7 +1078,11 @@ fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void* o, fl
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 1 || d < 1 || B > fa::kPagedMaxB) return 0;
   if (int64_t(B) * Hq * Nq >= (int64_t(1) << 31)) return 0;
-  return paged_ws_bytes(B, Hkv, Hq / Hkv * Nq, d, decode_sms());
+  // enough for either way of cutting the rows (which one it is depends on the page table's width too)
+  const int sms = decode_sms();
+  const size_t wide = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, 0), d, sms).total;
+  const size_t narrow = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, int64_t(1) << 40), d, sms).total;
+  return wide > narrow ? wide : narrow;
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, int64_t k_page_stride,

@@ -61,6 +61,16 @@ struct PagedParams {
   float scale_log2;
 };
 
+// How rows form tiles: in paged_wide_sm100.cuh a pair of tiles of tq positions each, all g heads; here
+// (for the merge) tiles of tq consecutive rows.
+struct WideParams {
+  PagedParams p;
+  int g;          // query heads per K/V head
+  int tq;
+  int n_pairs;    // tile pairs (tiles) per (sequence, K/V head)
+  uint64_t wait_ns;
+};
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {   // 16 bytes, zeros if not valid
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -685,16 +695,22 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
 // Merges the partials of one query row that several warps made, WPR warps of a CTA per row, four partials
 // in flight per warp.  Rows of a row tile that one warp had whole are done already.  Also writes the rows
 // of sequences without keys or without new tokens: O = 0, lse = -inf.
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, const int tile_rows) {
+template <int D, int WPR, bool WIDE>
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const WideParams q) {
+  const PagedParams& p = q.p;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int PER = D / 32, RPC = 8 / WPR;   // features per lane, rows per CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
   const unsigned row = blockIdx.x * RPC + warp / WPR;   // of [B, Hkv, R]; B Hq Nq < 2^31
   const bool real = row < unsigned(p.B) * p.Hkv * p.R;
   const unsigned bh = real ? row / p.R : 0, r = row % p.R, b = bh / p.Hkv;
-  const int has = p.plan[b + 1] - p.plan[b];
-  const int2 info = p.info[bh * p.row_tiles + r / tile_rows];
+  // its tile (or pair of tiles), the tile's row and the plan's entry
+  const int i = WIDE ? r % p.Nq : r;
+  const int tile = WIDE ? i / (2 * q.tq) : i / q.tq, tile_rows = WIDE ? 256 : q.tq;
+  const int srow = WIDE ? ((i / q.tq) & 1) * 128 + (i % q.tq) * q.g + r / p.Nq : i % q.tq;
+  const int64_t at = WIDE ? (int64_t)b * q.n_pairs + tile : b;
+  const int has = p.plan[at + 1] - p.plan[at];
+  const int2 info = p.info[(int64_t)bh * q.n_pairs + tile];
   float acc[PER], ms = -INFINITY, ls = 0.f;
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -718,7 +734,7 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
         const int w = w0 + u * WPR;
         ml[u] = make_float2(0.f, 0.f);
         if (w > info.y) continue;
-        const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * tile_rows + r % tile_rows;
+        const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * tile_rows + srow;
         ml[u] = p.part_ml[slot];
         if constexpr (PER == 4) {
           const float4 f = *reinterpret_cast<const float4*>(p.part_o + slot * D + lane * 4);

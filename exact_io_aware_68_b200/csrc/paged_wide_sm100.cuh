@@ -1,0 +1,768 @@
+// Attention over a paged key/value cache for sm_100a, many query rows per K/V head: chunks of prompts, drafted
+// tokens of wide groups.  Same operation and pools as paged_sm100.cuh.
+//
+// Bound: the tensor core (4 D flop per row and key against 4 D bytes per key: from about 250 rows on).
+// So this is the structure of the training forward (fwd_sm100.cuh): two 128-row query tiles A and B share every
+// 128-key block of K and V, tcgen05 MMAs accumulate S and O in TMEM, P goes back through TMEM, and one tile's
+// softmax runs while the tensor core works on the other.  What differs:
+//  * Rows.  A tile holds floor(128 / g) positions of all g = Hq / Hkv heads that share the K/V head, the heads of
+//    a position side by side, so that its rows see nearly the same keys.
+//  * Work.  A unit is one 128-key block of one (sequence, K/V head, tile pair).  fa_paged_plan_kernel forms the
+//    prefix of the pairs' block counts (causal pairs stop at their last visible key), and every CTA takes an equal,
+//    contiguous share of all units.  A pair that several CTAs share is merged from fp32 partials.
+//  * Pages.  One TMA box per page and 64-feature panel; a 128-key block is 128 / page of them.  Keys past the
+//    sequence's end are not loaded, and their rows of V are zeroed in shared memory (0 * stale would not be 0).
+//  * e4m3.  Four more warps turn the raw tiles into f16 (exact; NaN stays NaN), in the swizzled layout the MMA reads,
+//    and the queries too (each row times a power of two).  The page's key scale multiplies the finished scores, its
+//    value scale the probabilities.
+#pragma once
+#include "fwd_sm100.cuh"
+#include "paged_sm100.cuh"
+
+namespace fa {
+
+template <int D, bool FP8>
+struct WideLayout {
+  static constexpr int TILE = 128 * D * 2;         // bytes of one 128-row 16-bit tile
+  static constexpr int SUB = 128 * 128;            // one 64-column swizzle panel of a tile
+  static constexpr int RAW = 128 * D;              // bytes of one 128-row e4m3 tile
+  static constexpr int KST = FP8 ? 2 : (D == 128) ? 3 : 4;
+  static constexpr int VST = (D == 128 || FP8) ? 2 : 4;
+  static constexpr int RST = FP8 ? (D == 128 ? 2 : 4) : 0;   // raw tiles: K_0, V_0, K_1, ...
+  static constexpr int SST = 4;                    // scale sets (one per block)
+  static constexpr int QA_OFF = 0;
+  static constexpr int QB_OFF = QA_OFF + TILE;
+  static constexpr int K_OFF = QB_OFF + TILE;
+  static constexpr int V_OFF = K_OFF + KST * TILE;
+  static constexpr int RAW_OFF = V_OFF + VST * TILE;
+  static constexpr int SC_OFF = RAW_OFF + RST * RAW;            // [SST][2][8] fp32: K and V scales of the 16-key groups
+  static constexpr int QS_OFF = SC_OFF + (FP8 ? SST * 64 : 0);  // [2][2][128] fp32: score scale of the rows, by item parity
+  static constexpr int BAR_OFF = QS_OFF + (FP8 ? 2 * 2 * 128 * 4 : 0);
+  // q_full[2], q_empty[2], k_full, k_empty, v_full, v_empty, raw_full, raw_empty, s_full[2], p_full[2][2], o_fin[2],
+  // o_free[2], tail, fin
+  static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int START_OFF = MISC_OFF + 16;               // this CTA's first unit: b, h, pair, block, T
+  static constexpr int BYTES = START_OFF + 32;
+  __device__ static constexpr int s_col(int x) { return 128 * x; }
+  __device__ static constexpr int o_col(int x) { return 256 + D * x; }
+  static constexpr int TMEM_COLS = 512;
+  // Registers per thread of the warpgroups: softmax (2), producers and MMA issuer, converters.
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
+  static constexpr int SOFT_REGS = FP8 ? 176 : 200, IO_REGS = FP8 ? 80 : 104, CVT_REGS = 80;
+  static_assert(BYTES <= 232448, "shared memory budget");
+  static_assert(2 * SOFT_REGS + IO_REGS + (FP8 ? CVT_REGS : 0) <= THREADS / 128 * LAUNCH_REGS, "register budget");
+};
+
+template <int N>
+__device__ __forceinline__ void set_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void set_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" :: "n"(N) : "memory"); }
+
+// 4-D tiled load (no multicast) into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Blocks of one tile pair (x < 0) or of one of its tiles; kv: the keys that its rows see.
+__device__ __forceinline__ int wide_keys(const WideParams& q, int L, int n, int pair, int x) {
+  const int i0 = (2 * pair + (x > 0 ? 1 : 0)) * q.tq, i1 = (2 * pair + (x == 0 ? 1 : 2)) * q.tq;
+  if (i0 >= n) return 0;
+  return q.p.causal ? min(max(L - n + min(n, i1), 0), L) : L;
+}
+
+// Prefix of the block counts of all (sequence, tile pair)s, into p.plan.  One CTA.
+__global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const WideParams q) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ int sums[32];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int total = q.p.B * q.n_pairs;
+  if (tid == 0) carry = q.p.plan[0] = 0;
+  __syncthreads();
+  for (int base = 0; base < total; base += 1024) {
+    const int at = base + tid;
+    int v = 0;
+    if (at < total) {
+      const int b = at / q.n_pairs;
+      v = (wide_keys(q, paged_key_len(q.p, b), paged_new_len(q.p, b), at % q.n_pairs, -1) + 127) / 128;
+    }
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, s);
+      if (lane >= s) v += u;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      int u = sums[lane];
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, u, s);
+        if (lane >= s) u += t;
+      }
+      sums[lane] = u;
+    }
+    __syncthreads();
+    v += carry + (warp > 0 ? sums[warp - 1] : 0);
+    if (at < total) q.p.plan[at + 1] = v;
+    __syncthreads();
+    if (tid == 1023) carry = v;
+    __syncthreads();
+  }
+}
+
+// The largest i in [lo, hi) with f[i * step] * mul <= want; a whole warp, 32 candidates a round.
+__device__ __forceinline__ int wide_search(const int* f, int lo, int hi, int step, long long mul, long long want, int lane) {
+  while (hi - lo > 1) {
+    const int d = (hi - lo + 31) / 32, i = lo + lane * d;
+    const bool le = i < hi && f[(int64_t)i * step] * mul <= want;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lane 0 always holds
+    lo += last * d;
+    hi = min(hi, lo + d);
+  }
+  return lo;
+}
+
+// A CTA's walk over its units, segment by segment (a segment: consecutive blocks of one pair).
+struct WideWalk {
+  int b, h, pair, t, T;   // t: first block of the segment, T: blocks of the pair
+  int L, n, cnt;          // keys and new tokens of the sequence, blocks of the segment
+  long long left;         // units of the CTA from this segment on
+  __device__ __forceinline__ void fill(const WideParams& q) {
+    L = paged_key_len(q.p, b);
+    n = paged_new_len(q.p, b);
+    cnt = int(left < T - t ? left : T - t);
+  }
+  __device__ __forceinline__ void start(const WideParams& q, const int* first, long long units) {
+    b = first[0];
+    h = first[1];
+    pair = first[2];
+    t = first[3];
+    T = first[4];
+    left = units;
+    if (left > 0) fill(q);
+  }
+  __device__ __forceinline__ void next(const WideParams& q) {
+    left -= cnt;
+    if (left <= 0) return;
+    t = 0;
+    const int* f = q.p.plan;
+    const int b0 = b;
+    do {   // pairs with blocks; some are left
+      ++pair;
+      if (pair >= q.n_pairs || 2 * pair * q.tq >= n) {   // the pairs past the last token have none
+        pair = 0;
+        if (++h == q.p.Hkv) {
+          h = 0;
+          do ++b; while (b < q.p.B && f[(int64_t)(b + 1) * q.n_pairs] == f[(int64_t)b * q.n_pairs]);
+          if (b >= q.p.B) {   // (only if the lengths changed under the call)
+            left = 0;
+            return;
+          }
+          n = paged_new_len(q.p, b);
+        }
+      }
+      const int64_t at = (int64_t)b * q.n_pairs + pair;
+      T = f[at + 1] - f[at];
+    } while (T == 0);
+    if (b != b0) L = paged_key_len(q.p, b);
+    cnt = int(left < T ? left : T);
+  }
+  // blocks of tile x in this segment
+  __device__ __forceinline__ int blocks(const WideParams& q, int x) const {
+    return min(max((wide_keys(q, L, n, pair, x) + 127) / 128 - t, 0), cnt);
+  }
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__((WideLayout<D, FP8>::THREADS), 1)
+fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const WideParams q) {
+  using L = WideLayout<D, FP8>;
+  constexpr int KST = L::KST, VST = L::VST, RST = FP8 ? L::RST : 1;
+  const PagedParams& p = q.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) record_status(kStatusBadSmemAlign);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint64_t* q_full = bars;           // [2]: tile A, tile B
+  uint64_t* q_empty = q_full + 2;    // [2]
+  uint64_t* k_full = q_empty + 2;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* raw_full = v_empty + VST;
+  uint64_t* raw_empty = raw_full + L::RST;
+  uint64_t* s_full = raw_empty + L::RST;   // [2]
+  uint64_t* p_full = s_full + 2;      // [2][2]: tile, half of the keys
+  uint64_t* o_fin = p_full + 4;       // [2]: all PV of the segment done
+  uint64_t* o_free = o_fin + 2;       // [2]: the epilogue has read O
+  uint64_t* tail = o_free + 2;        // bf16: the V block that holds a sequence's end has landed
+  uint64_t* fin = tail + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+  int* first = reinterpret_cast<int*>(smem + L::START_OFF);
+
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], FP8 ? 4 : 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[2 * x], 4);
+      mbar_init(&p_full[2 * x + 1], 4);
+      mbar_init(&o_fin[x], 1);
+      mbar_init(&o_free[x], 4);
+    }
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(&k_full[s], FP8 ? 4 : 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], FP8 ? 4 : 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < L::RST; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+    }
+    mbar_init(tail, 1);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // the plan is a programmatic dependency: everything above overlaps it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long W = (long long)p.plan[p.B * q.n_pairs] * p.Hkv;
+  const int cta = int(blockIdx.x), sharers = paged_sharers(W, int(gridDim.x));
+  const long long u0 = cta < sharers ? paged_share(W, cta, sharers) : 0, u1 = cta < sharers ? paged_share(W, cta + 1, sharers) : 0;
+  if (warp == 0 && u0 < u1) {
+    const int b = wide_search(p.plan, 0, p.B, q.n_pairs, p.Hkv, u0, lane);
+    const int64_t at = (int64_t)b * q.n_pairs;
+    const int base = p.plan[at], sum = p.plan[at + q.n_pairs] - base;
+    const long long rem = u0 - (long long)base * p.Hkv;
+    const int h = int(rem / sum), v = base + int(rem % sum);
+    const int pair = wide_search(p.plan + at, 0, q.n_pairs, 1, 1, v, lane);
+    if (lane == 0) {
+      first[0] = b;
+      first[1] = h;
+      first[2] = pair;
+      first[3] = v - p.plan[at + pair];
+      first[4] = p.plan[at + pair + 1] - p.plan[at + pair];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{q.wait_ns, abort_flag};
+  WideWalk s;
+  s.start(q, first, u1 - u0);
+
+  // Pages of 128 keys from block t on: lane i looks at piece i (a page, or half of a 256-key page).
+  const int piece_rows = min(1 << p.page_shift, 128), pieces = 128 / piece_rows;
+  auto piece_page = [&](const WideWalk& w, int j, int i) -> int {   // its page, n_pages (zeros) if bad, -1 past the end
+    const int key = (w.t + j) * 128 + i * piece_rows;
+    if (i >= pieces || key >= w.L) return -1;
+    const int id = __ldg(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift));
+    if (unsigned(id) >= unsigned(p.n_pages)) {
+      record_status(kStatusRange);
+      return p.n_pages;
+    }
+    return id;
+  };
+
+  if (warp >= 8 && warp < 12) {
+    set_regs_dec<L::IO_REGS>();
+    if (warp == 11 && !FP8) {
+      // =========================================================== producer of the Q tiles
+      if (lane == 0) {
+        prefetch_tmap(&tm_q);
+        int nq[2] = {0, 0};   // Q tiles delivered, per tile
+        bool ok = true;
+        for (; ok && s.left > 0; s.next(q)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (s.blocks(q, x) == 0) continue;
+            if (nq[x] >= 1 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc)) { ok = false; break; }
+            mbar_arrive_expect_tx(&q_full[x], D * 2 * q.g * q.tq);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(smem + (x ? L::QB_OFF : L::QA_OFF) + c * L::SUB, &tm_q, &q_full[x], c * 64, 0,
+                          (2 * s.pair + x) * q.tq, s.b * p.Hkv + s.h);
+            ++nq[x];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (nq[x] >= 1) mbar_drain(&q_full[x], (nq[x] - 1) & 1, q.wait_ns);
+      }
+      __syncwarp();
+    } else if (!FP8 && (warp == 8 || warp == 10)) {
+      // =========================================================== producers of the K (warp 8) and V (warp 10) rings
+      const bool is_k = (warp == 8);
+      const int NS = is_k ? KST : VST;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      uint8_t* ring = smem + (is_k ? L::K_OFF : L::V_OFF);
+      if (lane == 0) prefetch_tmap(map);
+      int g = 0, tails = 0;   // blocks delivered so far; those with a sequence's end
+      bool ok = true;
+      for (; ok && s.left > 0; s.next(q)) {
+        const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+        for (int j = 0; j < n_max; ++j, ++g) {
+          const int st = g % NS;
+          const int page = piece_page(s, j, lane);
+          const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+          const int key0 = (s.t + j) * 128;
+          const bool ends = !is_k && key0 + 128 > s.L;
+          if (!__all_sync(0xffffffffu, g < NS || mbar_wait(&empty[st], ((g / NS) - 1) & 1, wc))) { ok = false; break; }
+          uint64_t* bar = ends ? tail : &full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * piece_rows * D * 2);
+          __syncwarp();
+          if (page >= 0) {
+            const int y = (key0 + lane * piece_rows) & ((1 << p.page_shift) - 1);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(ring + st * L::TILE + c * L::SUB + lane * piece_rows * 128, map, bar, c * 64, y, s.h, page);
+          }
+          if (ends) {   // rows past the end: zeros, before the block is handed on
+            if (!__all_sync(0xffffffffu, mbar_wait(tail, tails & 1, wc))) { ok = false; break; }
+            ++tails;
+            for (int i = lane; i < (key0 + 128 - s.L) * (D / 8); i += 32) {
+              const int row = s.L - key0 + i / (D / 8), c = i % (D / 8);
+              *reinterpret_cast<uint4*>(ring + st * L::TILE + (c >> 3) * L::SUB + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+        }
+      }
+      if (lane == 0) {   // every copy started here lands before the CTA releases its shared memory
+        if (!ok && !is_k) mbar_drain(tail, tails & 1, q.wait_ns);   // a copy of an unfinished tail block, if any
+        for (int j = max(0, g - NS); j < g; ++j) mbar_drain(&full[j % NS], (j / NS) & 1, q.wait_ns);
+      }
+      __syncwarp();
+    } else if (FP8 && warp == 8) {
+      // =========================================================== producer of the raw tiles
+      if (lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+      }
+      int g = 0;
+      bool ok = true;
+      for (; ok && s.left > 0; s.next(q)) {
+        const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+        for (int j = 0; ok && j < n_max; ++j) {
+          const int page = piece_page(s, j, lane);
+          const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+          const int y = ((s.t + j) * 128 + lane * piece_rows) & ((1 << p.page_shift) - 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++g) {
+            const int st = g % RST;
+            if (!__all_sync(0xffffffffu, g < RST || mbar_wait(&raw_empty[st], ((g / RST) - 1) & 1, wc))) { ok = false; break; }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], __popc(have) * piece_rows * D);
+            __syncwarp();
+            if (page >= 0)
+              tma_load_4d(smem + L::RAW_OFF + st * L::RAW + lane * piece_rows * D, kv ? &tm_v : &tm_k, &raw_full[st], 0, y, s.h, page);
+          }
+        }
+      }
+      if (lane == 0)
+        for (int j = max(0, g - RST); j < g; ++j) mbar_drain(&raw_full[j % RST], (j / RST) & 1, q.wait_ns);
+      __syncwarp();
+    } else if (warp == 9) {
+      // =========================================================== MMA issuer (whole warp, elect.sync)
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+      constexpr uint32_t kType = FP8 ? (1u << 7) | (1u << 10) : 0u;   // e4m3: f16 operands (format 0) instead of bf16 (1)
+      constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false) & ~kType;   // Q: K-major, K: K-major
+      constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true) & ~kType;     // P: TMEM, V: MN-major
+      const uint32_t s0 = smem_u32(smem) >> 4;
+      constexpr uint32_t kHi = sdesc_sw128_hi(1024), kKM = sdesc_lbo(16), kMN = sdesc_lbo(L::SUB);
+      int gk = 0;                // blocks consumed (K and V alike)
+      int nb[2] = {0, 0};        // blocks of each tile so far: phase of p_full
+      int ni[2] = {0, 0};        // segments with work for each tile so far: phase of q_full, o_free
+      bool ok = true;
+      for (; ok && s.left > 0; s.next(q)) {
+        const int n_x[2] = {s.blocks(q, 0), s.blocks(q, 1)};
+        const int n_max = max(n_x[0], n_x[1]);
+        if (n_max == 0) continue;
+        auto issue_s = [&](int x, int kst) {   // S_x = Q_x K^T
+          const uint32_t q_lo = s0 + uint32_t((x ? L::QB_OFF : L::QA_OFF) >> 4) + kKM;
+          const uint32_t k_lo = s0 + uint32_t((L::K_OFF + kst * L::TILE) >> 4) + kKM;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::SUB + (kk & 3) * 32) >> 4;
+            mma_ss_elect(tmem + L::s_col(x), sdesc_join(q_lo + off, kHi), sdesc_join(k_lo + off, kHi), kIdS, kk > 0 ? 1u : 0u);
+          }
+        };
+        auto issue_pv_half = [&](int x, int vst, int h, uint32_t acc0) {   // O_x += P_x[keys of half h] V[same keys]
+          const uint32_t v_lo = s0 + uint32_t((L::V_OFF + vst * L::TILE) >> 4) + kMN;
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_ts_elect(tmem + L::o_col(x), tmem + L::s_col(x) + kk * 8, sdesc_join(v_lo + kk * (2048 >> 4), kHi), kIdPV,
+                         kk > 0 ? 1u : acc0);
+        };
+        if (!wait(&k_full[gk % KST], (gk / KST) & 1)) { ok = false; break; }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (n_x[x] == 0) continue;
+          if (!wait(&q_full[x], ni[x] & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(x, gk % KST);
+          mma_commit_elect(&s_full[x]);
+          if (n_x[x] == 1) mma_commit_elect(&q_empty[x]);   // the next segment's Q_x may come now
+        }
+        if (!ok) break;
+        mma_commit_elect(&k_empty[gk % KST]);
+        for (int j = 0; ok && j < n_max; ++j) {
+          const int vst = (gk + j) % VST, kst1 = (gk + j + 1) % KST;
+          if (!wait(&v_full[vst], ((gk + j) / VST) & 1)) { ok = false; break; }
+          bool have_k = false;   // K_{j+1} resident
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= n_x[x]) continue;
+            // the first PV of a segment overwrites O: the previous segment's epilogue must have read it
+            if (j == 0 && ni[x] >= 1 && !wait(&o_free[x], (ni[x] - 1) & 1)) { ok = false; break; }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!wait(&p_full[2 * x + h], (nb[x] + j) & 1)) { ok = false; break; }
+              tc_fence_after();
+              issue_pv_half(x, vst, h, j > 0 ? 1u : 0u);
+            }
+            if (!ok) break;
+            if (j + 1 < n_x[x]) {
+              if (!have_k) {
+                if (!wait(&k_full[kst1], ((gk + j + 1) / KST) & 1)) { ok = false; break; }
+                tc_fence_after();
+                have_k = true;
+              }
+              issue_s(x, kst1);
+              mma_commit_elect(&s_full[x]);
+              if (j + 2 == n_x[x]) mma_commit_elect(&q_empty[x]);
+            } else {
+              mma_commit_elect(&o_fin[x]);
+            }
+          }
+          if (!ok) break;
+          mma_commit_elect(&v_empty[vst]);                       // V_j: both tiles' PV issued
+          if (j + 1 < n_max) mma_commit_elect(&k_empty[kst1]);   // K_{j+1}: both tiles' S issued
+        }
+        gk += n_max;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          nb[x] += n_x[x];
+          ni[x] += (n_x[x] > 0);
+        }
+      }
+      mma_commit_elect(fin);   // completes when every MMA issued above has finished
+      if (lane == 0) mbar_drain(fin, 0, q.wait_ns);
+      __syncwarp();
+    }
+  } else if (FP8 && warp >= 12) {
+    // =========================================================== converters: e4m3 -> f16, queries bf16 -> f16
+    set_regs_dec<L::CVT_REGS>();
+    const int ct = tid - 384;
+    float* scales = reinterpret_cast<float*>(smem + L::SC_OFF);
+    float* qscale = reinterpret_cast<float*>(smem + L::QS_OFF);
+    int g = 0, gb = 0;        // raw tiles, blocks so far
+    int nq[2] = {0, 0};
+    bool ok = true;
+    for (; ok && s.left > 0; s.next(q)) {
+      const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (s.blocks(q, x) == 0) continue;
+        if (!__all_sync(0xffffffffu, nq[x] < 1 || mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc))) { ok = false; break; }
+        const int i = (2 * s.pair + x) * q.tq + ct / q.g, jj = ct % q.g;
+        const bool real = ct < q.g * q.tq && i < p.Nq;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + i) * D);
+        float mx = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+        }
+        // each row times a power of two that puts its largest element into [2^14, 2^15)
+        const int ex = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
+        const bool scaled = mx > 0.f && mx < INFINITY;
+        const float up = scaled ? __uint_as_float(uint32_t(127 + 14 - ex) << 23) : 1.f;
+        qscale[((nq[x] & 1) * 2 + x) * 128 + ct] = p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 14 + ex) << 23) : 1.f);
+        uint8_t* dst = smem + (x ? L::QB_OFF : L::QA_OFF) + ct * 128;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * L::SUB + (((c & 7) ^ (ct & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[x]);
+        ++nq[x];
+      }
+      if (!ok) break;
+      for (int j = 0; ok && j < n_max; ++j, ++gb) {
+        const int key0 = (s.t + j) * 128;
+        float my_scale = 0.f;   // threads 0-15: K and V scale of 16-key group ct & 7
+        if (ct < 16) {
+          const int key = key0 + 16 * (ct & 7);
+          if (key < s.L) {
+            const int id = __ldg(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift));
+            if (unsigned(id) < unsigned(p.n_pages)) my_scale = __ldg((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+          const int st = g % RST, NS = kv ? VST : KST, dst_st = gb % NS;
+          uint64_t* empty = kv ? &v_empty[dst_st] : &k_empty[dst_st];
+          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (g / RST) & 1, wc))) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, gb < NS || mbar_wait(empty, ((gb / NS) - 1) & 1, wc))) { ok = false; break; }
+          if (kv == 0 && ct < 16) scales[(gb % L::SST) * 16 + ct] = my_scale;
+          const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
+          uint8_t* dst = smem + (kv ? L::V_OFF : L::K_OFF) + dst_st * L::TILE;
+          constexpr int CPR = D / 16;   // raw 16-byte chunks per key
+#pragma unroll 4
+          for (int i = 0; i < CPR; ++i) {
+            const int id = i * 128 + ct, row = id / CPR, c = id % CPR;
+            const uint4 w = *reinterpret_cast<const uint4*>(raw + id * 16);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = e4m3x2_to_f16x2(u[e]);
+              o[2 * e + 1] = e4m3x2_to_f16x2(u[e] >> 16);
+            }
+            if (key0 + row >= s.L) {   // past the end: what lies there is nobody's
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = 0u;
+            }
+            uint8_t* d = dst + (c >> 2) * L::SUB + row * 128;
+            // 16-bit chunks 2c and 2c + 1 of the row; lanes of the second panel store them in the other order, so
+            // that 8 lanes meet 8 different banks
+            const int z = c >> 2;
+            const int ca = ((2 * c + z) & 7) ^ (row & 7), cb = ((2 * c + 1 - z) & 7) ^ (row & 7);
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(d + (ca << 4)) = z ? hi : lo;
+            *reinterpret_cast<uint4*>(d + (cb << 4)) = z ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[st]);
+            mbar_arrive(kv ? &v_full[dst_st] : &k_full[dst_st]);
+          }
+        }
+      }
+    }
+  } else {
+    // =========================================================== softmax / epilogue (warps 0-7)
+    set_regs_inc<L::SOFT_REGS>();
+    const int x = warp >> 2;   // tile
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t s_addr = lane_base + L::s_col(x);
+    const uint32_t o_addr = lane_base + L::o_col(x);
+    const int ii = r / q.g, jj = r % q.g;
+    int nb = 0, ni = 0, gb = 0;   // blocks and segments of this tile, blocks of the CTA so far
+    bool ok = true, first_seg = true;
+    for (; ok && s.left > 0; s.next(q), first_seg = false) {
+      const int n = s.blocks(q, x);
+      const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
+      const bool stored = ii < q.tq && qi < p.Nq;
+      const int lim = stored && qi < s.n ? (p.causal ? max(s.L - s.n + qi + 1, 0) : s.L) : 0;   // keys < lim allowed
+      const int lim_lo = p.causal ? s.L - s.n + i0 + 1 : s.L;                                // the tile's smallest
+      float sl2 = p.scale_log2;
+      float m_ref = -INFINITY;   // reference max, exp2 domain
+      float l = 0.f;
+      float vref = 6.0185311e-36f;   // e4m3: the largest value scale so far (2^-117), O is in units of it
+      for (int j = 0; j < n; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], (nb + j) & 1, wc))) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(s_addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld32(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+        tmem_ld32(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * h]));
+        const volatile float* sc = reinterpret_cast<const volatile float*>(smem + L::SC_OFF) + ((gb + j) % L::SST) * 16;
+        float vmove = 1.f, unit = 1.f;
+        if constexpr (FP8) {
+          if (j == 0) sl2 = reinterpret_cast<const volatile float*>(smem + L::QS_OFF)[((ni & 1) * 2 + x) * 128 + r];
+          float vmax = vref;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float ks = sc[u];
+            vmax = fmaxf(vmax, sc[8 + u]);
+#pragma unroll
+            for (int c = 16 * u; c < 16 * u + 16; c += 2) {
+              float a, b;
+              f2_split(f2_mul(f2_make(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2_make(ks, ks)), a, b);
+              sr[c] = __float_as_uint(a);
+              sr[c + 1] = __float_as_uint(b);
+            }
+          }
+          if (vmax > vref) {
+            vmove = vref / vmax;
+            vref = vmax;
+          }
+          unit = kPagedPScale / vref;
+        }
+
+        const int k0 = (s.t + j) * 128;
+        if (k0 + 128 > min(lim_lo, s.L)) {   // block straddles a mask edge
+          const int keep = lim - k0;         // columns < keep are kept
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= keep) sr[c] = __float_as_uint(-INFINITY);
+        }
+        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent chains
+#pragma unroll
+        for (int c = 0; c < 128; c += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mxv[u] = max3f(mxv[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
+        const float m_cand = fmaxf(max3f(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
+        float alpha = 1.f;
+        if (m_cand > m_ref + kPagedRescale) {
+          alpha = ex2_approx(m_ref - m_cand);
+          m_ref = m_cand;
+        }
+        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+        const uint64_t sl2x2 = f2_make(sl2, sl2), negm2 = f2_make(-m_use, -m_use);
+        uint64_t rs2 = f2_make(0.f, 0.f);
+        const float o_move = alpha * vmove;
+        float vs = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // two halves of 64 keys; the MMA takes each half as soon as it is ready
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = 32 * h + e;   // pair index: keys 2c, 2c + 1
+            uint64_t pp = exp2_pair(sr[2 * c], sr[2 * c + 1], sl2x2, negm2);
+            rs2 = f2_add(rs2, pp);
+            float p0, p1;
+            if constexpr (FP8) {
+              if ((e & 7) == 0) vs = sc[8 + (c >> 3)] * unit;   // 8 pairs: one 16-key group
+              f2_split(f2_mul(pp, f2_make(vs, vs)), p0, p1);
+              pk[e] = pack_f16x2(p0, p1);
+            } else {
+              f2_split(pp, p0, p1);
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+          }
+          // P over the score columns already read; O already holds PV up to block j-1
+          tmem_st32(s_addr + 32 * h, pk);
+          if (h == 0 && j >= 1 && __any_sync(0xffffffffu, o_move != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t orr[32];
+              tmem_ld32(o_addr + c * 32, orr);
+              tmem_ld_wait();
+              reg_fence32(orr);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * o_move);
+              tmem_st32(o_addr + c * 32, orr);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
+        }
+        float rs0, rs1;
+        f2_split(rs2, rs0, rs1);
+        l = l * alpha + (rs0 + rs1);
+      }
+      if (!ok) break;
+      gb += max(s.blocks(q, 0), s.blocks(q, 1));
+
+      // ---- epilogue: O / l in bf16 and lse, or the segment's partial
+      const bool whole = s.t == 0 && s.cnt == s.T;
+      const int64_t out = ((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + qi;
+      const int64_t slot = (2 * (int64_t)cta + (first_seg ? 0 : 1)) * 256 + 128 * x + r;
+      if (tid == 0) {
+        int2* info = p.info + (s.b * p.Hkv + s.h) * q.n_pairs + s.pair;
+        if (s.t + s.cnt == s.T) info->y = whole ? -1 : cta;
+        if (s.t == 0) info->x = 2 * cta + (first_seg ? 0 : 1);
+      }
+      if (lim == 0 || n == 0) l = 0.f;
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_fin[x], ni & 1, wc))) { ok = false; break; }
+        tc_fence_after();
+      }
+      const float f = l != 0.f ? (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? 1.f / l : 1.f) : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t orr[32];
+        if (n > 0) {
+          tmem_ld32(o_addr + c * 32, orr);
+          tmem_ld_wait();
+          reg_fence32(orr);
+        }
+        if (!stored) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = l != 0.f ? pack_bf16x2(__uint_as_float(orr[2 * e]) * f, __uint_as_float(orr[2 * e + 1]) * f) : 0u;
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + 32 * c);   // (o is 16-byte aligned)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        } else if (l != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * f);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            st_global_v8(p.part_o + slot * D + 32 * c + e, orr[e], orr[e + 1], orr[e + 2], orr[e + 3], orr[e + 4], orr[e + 5],
+                         orr[e + 6], orr[e + 7]);
+        }
+      }
+      if (n > 0) {   // O has been read: the next segment's first PV may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[x]);
+      }
+      if (stored) {
+        if (whole)
+          p.lse[out] = l != 0.f ? (m_ref + lg2_approx(l)) * kPagedLn2 : -INFINITY;
+        else
+          p.part_ml[slot] = make_float2(m_ref, l);
+      }
+      nb += n;
+      ni += (n > 0);
+    }
+  }
+
+  // ---- teardown: every role has drained its asynchronous work
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+}  // namespace fa

@@ -134,6 +134,12 @@ ATTENTION = [
     (1, 1, 8, 16, 64, 64, [500], None, False),
     (33, 1, 2, 1, 128, 16, [16 * (i % 5) + i for i in range(33)], None, True),
     (2, 1, 1, 2, 64, 16, [1, 3], [2, 2], True),     # a query before position 0 sees nothing
+    (2, 1, 3, 300, 128, 64, [300, 1000], [300, 211], True),
+    (1, 1, 8, 40, 64, 16, [5000], None, True),
+    (5, 2, 4, 33, 128, 32, [33, 0, 128, 129, 700], [33, 0, 1, 33, 20], True),
+    (2, 1, 1, 600, 64, 256, [600, 1025], None, False),
+    (3, 1, 20, 9, 128, 128, [4, 200, 9], [9, 9, 2], True),
+    (1, 1, 130, 1, 64, 16, [77], None, True),       # more heads in a group than a tile has rows
 ]
 
 
