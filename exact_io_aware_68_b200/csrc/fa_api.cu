@@ -519,15 +519,17 @@ fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, 
 
 // Warps per row: 8 while that makes at most 4 CTAs per SM (few rows, many partials each), 4 while it
 // makes at most 16, else 1.
-template <int D, bool WIDE>
-fa_status launch_paged_combine(const fa::WideParams& q, int sms, cudaStream_t s) {
-  const long long rows = (long long)q.p.B * q.p.Hkv * q.p.R;
+template <int D>
+fa_status launch_paged_combine(const fa::PagedParams& p, int tile_rows, int sms, cudaStream_t s) {
+  const long long rows = (long long)p.B * p.Hkv * p.R;
   const char* what = "fa_fwd_paged combine kernel launch";
   if (rows <= 4LL * sms)
-    return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 8, WIDE>, unsigned(rows), 256, 0, s, what, q);
+    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 8>, unsigned(rows), 256, 0, s, what, p, tile_rows);
   if (rows <= 32LL * sms)
-    return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 4, WIDE>, unsigned((rows + 1) / 2), 256, 0, s, what, q);
-  return launch_dependent<fa::WideParams>(fa::fa_paged_combine_kernel<D, 1, WIDE>, unsigned((rows + 7) / 8), 256, 0, s, what, q);
+    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 4>, unsigned((rows + 1) / 2), 256, 0, s, what, p,
+                                                  tile_rows);
+  return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 1>, unsigned((rows + 7) / 8), 256, 0, s, what, p,
+                                                tile_rows);
 }
 
 template <int D, bool FP8, int NG>
@@ -540,7 +542,7 @@ fa_status launch_paged(fa::WideParams q, int sms, cudaStream_t s) {
   if (st != FA_OK) return st;
   fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(q.p.B), s>>>(q.p);
   if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
-  return launch_paged_combine<D, false>(q, sms, s);
+  return launch_paged_combine<D>(q.p, 8 * NG, sms, s);
 }
 
 // Pool of pages as {d, page_size, Hkv, n_pages}, loaded page by page (at most 128 rows): 64 features with the
@@ -594,7 +596,9 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
       kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mk, mv, q);
   if (st != FA_OK) return st;
-  return launch_paged_combine<D, true>(q, sms, s);
+  // B Hkv pairs < 2^29: B Hq Nq < 2^31 and a pair has at least g positions' rows
+  return launch_dependent<fa::WideParams>(fa::fa_paged_wide_combine_kernel<D>, unsigned(p.B) * p.Hkv * q.n_pairs * 4, 256, 0, s,
+                                          "fa_fwd_paged combine kernel launch", q);
 }
 
 fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -61,16 +61,6 @@ struct PagedParams {
   float scale_log2;
 };
 
-// How rows form tiles: in paged_wide_sm100.cuh a pair of tiles of tq positions each, all g heads; here
-// (for the merge) tiles of tq consecutive rows.
-struct WideParams {
-  PagedParams p;
-  int g;          // query heads per K/V head
-  int tq;
-  int n_pairs;    // tile pairs (tiles) per (sequence, K/V head)
-  uint64_t wait_ns;
-};
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {   // 16 bytes, zeros if not valid
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -692,55 +682,43 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   }
 }
 
-// Merges the partials of one query row that several warps made, WPR warps of a CTA per row, four partials
-// in flight per warp.  Rows of a row tile that one warp had whole are done already.  Also writes the rows
-// of sequences without keys or without new tokens: O = 0, lse = -inf.
-template <int D, int WPR, bool WIDE>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const WideParams q) {
-  const PagedParams& p = q.p;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int PER = D / 32, RPC = 8 / WPR;   // features per lane, rows per CTA
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-  const unsigned row = blockIdx.x * RPC + warp / WPR;   // of [B, Hkv, R]; B Hq Nq < 2^31
-  const bool real = row < unsigned(p.B) * p.Hkv * p.R;
-  const unsigned bh = real ? row / p.R : 0, r = row % p.R, b = bh / p.Hkv;
-  // its tile (or pair of tiles), the tile's row and the plan's entry
-  const int i = WIDE ? r % p.Nq : r;
-  const int tile = WIDE ? i / (2 * q.tq) : i / q.tq, tile_rows = WIDE ? 256 : q.tq;
-  const int srow = WIDE ? ((i / q.tq) & 1) * 128 + (i % q.tq) * q.g + r / p.Nq : i % q.tq;
-  const int64_t at = WIDE ? (int64_t)b * q.n_pairs + tile : b;
-  const int has = p.plan[at + 1] - p.plan[at];
-  const int2 info = p.info[(int64_t)bh * q.n_pairs + tile];
-  float acc[PER], ms = -INFINITY, ls = 0.f;
+// Running merge of partials: m, l and a lane's features of O.
+template <int PER>
+struct PagedMerge {
+  float acc[PER], m, l;
+  __device__ __forceinline__ PagedMerge() : m(-INFINITY), l(0.f) {
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  auto add = [&](float m, float l, const float* x) {
-    if (l == 0.f) return;   // no key seen there (its m may be -inf)
-    const float mn = fmaxf(ms, m);
-    const float a = ms == -INFINITY ? 0.f : ex2_approx(ms - mn), c = ex2_approx(m - mn);
-    ls = ls * a + l * c;
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(float m1, float l1, const float* x) {
+    if (l1 == 0.f) return;   // no key seen there (its m may be -inf)
+    const float mn = fmaxf(m, m1);
+    const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn), c = ex2_approx(m1 - mn);
+    l = l * a + l1 * c;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + x[e] * c;
-    ms = mn;
-  };
-  const bool whole = has > 0 && info.y < 0;
-  if (real && has > 0 && !whole) {
-    const int first = info.x >> 1;   // the first warp's slot may be its second, the others' is their first
-    for (int w0 = first + sub; w0 <= info.y; w0 += 4 * WPR) {
+    m = mn;
+  }
+  // partials sub, sub + step, ... of one row, four in flight; the first partial may be its warp's (CTA's) second slot,
+  // the others are the first ones of theirs
+  __device__ __forceinline__ void gather(const PagedParams& p, int2 info, int sub, int step, int rows, int srow, int lane) {
+    const int first = info.x >> 1;
+    for (int w0 = first + sub; w0 <= info.y; w0 += 4 * step) {
       float2 ml[4];
       float x[4][PER];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int w = w0 + u * WPR;
+        const int w = w0 + u * step;
         ml[u] = make_float2(0.f, 0.f);
         if (w > info.y) continue;
-        const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * tile_rows + srow;
+        const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * rows + srow;
         ml[u] = p.part_ml[slot];
+        const float* from = p.part_o + slot * (32 * PER) + lane * PER;
         if constexpr (PER == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(p.part_o + slot * D + lane * 4);
+          const float4 f = *reinterpret_cast<const float4*>(from);
           x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
         } else {
-          const float2 f = *reinterpret_cast<const float2*>(p.part_o + slot * D + lane * 2);
+          const float2 f = *reinterpret_cast<const float2*>(from);
           x[u][0] = f.x; x[u][1] = f.y;
         }
       }
@@ -748,25 +726,45 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const WideParams 
       for (int u = 0; u < 4; ++u) add(ml[u].x, ml[u].y, x[u]);
     }
   }
+  __device__ __forceinline__ void store(const PagedParams& p, int64_t row, int lane) const {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * (32 * PER) + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) p.lse[row] = l != 0.f ? (m + lg2_approx(l)) * kPagedLn2 : -INFINITY;
+  }
+};
+
+// Merges the partials of query rows that several warps made, WPR warps of a CTA per row.  Rows of a row
+// tile that one warp had whole are done already.  Also writes the rows of sequences without keys or
+// without new tokens: O = 0, lse = -inf.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, const int tile_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int PER = D / 32, RPC = 8 / WPR;   // features per lane, rows per CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const unsigned row = blockIdx.x * RPC + warp / WPR;   // of [B, Hkv, R]; B Hq Nq < 2^31
+  const bool real = row < unsigned(p.B) * p.Hkv * p.R;
+  const unsigned bh = real ? row / p.R : 0, r = row % p.R, b = bh / p.Hkv;
+  const bool has = p.plan[b + 1] > p.plan[b];
+  const int2 info = p.info[(int64_t)bh * p.row_tiles + r / tile_rows];
+  const bool whole = has && info.y < 0;
+  PagedMerge<PER> a;
+  if (real && has && !whole) a.gather(p, info, sub, WPR, tile_rows, r % tile_rows, lane);
   if constexpr (WPR > 1) {
     __shared__ float sm[8], sl[8], so[8][D];
     if (lane == 0) {
-      sm[warp] = ms;
-      sl[warp] = ls;
+      sm[warp] = a.m;
+      sl[warp] = a.l;
     }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = acc[e];
+    for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = a.acc[e];
     __syncthreads();
     if (sub != 0) return;
 #pragma unroll
-    for (int y = 1; y < WPR; ++y) add(sm[warp + y], sl[warp + y], &so[warp + y][lane * PER]);
+    for (int y = 1; y < WPR; ++y) a.add(sm[warp + y], sl[warp + y], &so[warp + y][lane * PER]);
   }
-  if (!real || whole) return;
-  const float inv = ls != 0.f ? 1.f / ls : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)row * D + lane * PER);
-#pragma unroll
-  for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) p.lse[row] = ls != 0.f ? (ms + lg2_approx(ls)) * kPagedLn2 : -INFINITY;
+  if (real && !whole) a.store(p, row, lane);
 }
 
 }  // namespace fa

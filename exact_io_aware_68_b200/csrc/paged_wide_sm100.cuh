@@ -21,6 +21,22 @@
 
 namespace fa {
 
+struct WideParams {
+  PagedParams p;
+  int g;          // query heads per K/V head, <= 128
+  int tq;         // positions per tile: floor(128 / g)
+  int n_pairs;    // tile pairs per (sequence, K/V head)
+  uint64_t wait_ns;
+};
+
+// A segment: consecutive blocks of one pair, as much of it as falls into the CTA's share.
+struct WideSeg {
+  int b, h, pair, t, T;   // t: its first block, T: blocks of the pair
+  int L, n, cnt;          // keys and new tokens of the sequence, blocks of the segment (0: the share is done)
+  int blocks[2];          // blocks of either tile in it; their maximum is cnt
+  int first, pad;         // the CTA's first segment
+};
+
 template <int D, bool FP8>
 struct WideLayout {
   static constexpr int TILE = 128 * D * 2;         // bytes of one 128-row 16-bit tile
@@ -39,16 +55,18 @@ struct WideLayout {
   static constexpr int QS_OFF = SC_OFF + (FP8 ? SST * 64 : 0);  // [2][2][128] fp32: score scale of the rows, by item parity
   static constexpr int BAR_OFF = QS_OFF + (FP8 ? 2 * 2 * 128 * 4 : 0);
   // q_full[2], q_empty[2], k_full, k_empty, v_full, v_empty, raw_full, raw_empty, s_full[2], p_full[2][2], o_fin[2],
-  // o_free[2], tail, fin
-  static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2;
+  // o_free[2], tail, fin, seg_full, seg_empty
+  static constexpr int SEGS = 4;                   // segments scheduled ahead
+  static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2 + 2 * SEGS;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int START_OFF = MISC_OFF + 16;               // this CTA's first unit: b, h, pair, block, T
-  static constexpr int BYTES = START_OFF + 32;
+  static constexpr int SEG_OFF = MISC_OFF + 16;
+  static constexpr int BYTES = SEG_OFF + SEGS * int(sizeof(WideSeg));
   __device__ static constexpr int s_col(int x) { return 128 * x; }
   __device__ static constexpr int o_col(int x) { return 256 + D * x; }
   static constexpr int TMEM_COLS = 512;
   // Registers per thread of the warpgroups: softmax (2), producers and MMA issuer, converters.
   static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int READERS = FP8 ? 14 : 11;   // warps that read the segments: all but the scheduling one and idle ones
   static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
   static constexpr int SOFT_REGS = FP8 ? 176 : 200, IO_REGS = FP8 ? 80 : 104, CVT_REGS = 80;
   static_assert(BYTES <= 232448, "shared memory budget");
@@ -129,54 +147,43 @@ __device__ __forceinline__ int wide_search(const int* f, int lo, int hi, int ste
   return lo;
 }
 
-// A CTA's walk over its units, segment by segment (a segment: consecutive blocks of one pair).
+// The walk over a CTA's share, by the scheduling warp.
 struct WideWalk {
-  int b, h, pair, t, T;   // t: first block of the segment, T: blocks of the pair
-  int L, n, cnt;          // keys and new tokens of the sequence, blocks of the segment
-  long long left;         // units of the CTA from this segment on
+  WideSeg s;
+  int left;   // units of the share from this segment on
   __device__ __forceinline__ void fill(const WideParams& q) {
-    L = paged_key_len(q.p, b);
-    n = paged_new_len(q.p, b);
-    cnt = int(left < T - t ? left : T - t);
-  }
-  __device__ __forceinline__ void start(const WideParams& q, const int* first, long long units) {
-    b = first[0];
-    h = first[1];
-    pair = first[2];
-    t = first[3];
-    T = first[4];
-    left = units;
-    if (left > 0) fill(q);
+    s.cnt = min(left, s.T - s.t);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      s.blocks[x] = min(max((wide_keys(q, s.L, s.n, s.pair, x) + 127) / 128 - s.t, 0), s.cnt);
   }
   __device__ __forceinline__ void next(const WideParams& q) {
-    left -= cnt;
+    left -= s.cnt;
+    s.cnt = 0;
+    s.first = 0;
     if (left <= 0) return;
-    t = 0;
+    s.t = 0;
     const int* f = q.p.plan;
-    const int b0 = b;
+    const int b0 = s.b;
     do {   // pairs with blocks; some are left
-      ++pair;
-      if (pair >= q.n_pairs || 2 * pair * q.tq >= n) {   // the pairs past the last token have none
-        pair = 0;
-        if (++h == q.p.Hkv) {
-          h = 0;
-          do ++b; while (b < q.p.B && f[(int64_t)(b + 1) * q.n_pairs] == f[(int64_t)b * q.n_pairs]);
-          if (b >= q.p.B) {   // (only if the lengths changed under the call)
+      ++s.pair;
+      if (s.pair >= q.n_pairs || 2 * s.pair * q.tq >= s.n) {   // the pairs past the last token have none
+        s.pair = 0;
+        if (++s.h == q.p.Hkv) {
+          s.h = 0;
+          do ++s.b; while (s.b < q.p.B && f[(int64_t)(s.b + 1) * q.n_pairs] == f[(int64_t)s.b * q.n_pairs]);
+          if (s.b >= q.p.B) {   // (only if the lengths changed under the call)
             left = 0;
             return;
           }
-          n = paged_new_len(q.p, b);
+          s.n = paged_new_len(q.p, s.b);
         }
       }
-      const int64_t at = (int64_t)b * q.n_pairs + pair;
-      T = f[at + 1] - f[at];
-    } while (T == 0);
-    if (b != b0) L = paged_key_len(q.p, b);
-    cnt = int(left < T ? left : T);
-  }
-  // blocks of tile x in this segment
-  __device__ __forceinline__ int blocks(const WideParams& q, int x) const {
-    return min(max((wide_keys(q, L, n, pair, x) + 127) / 128 - t, 0), cnt);
+      const int64_t at = (int64_t)s.b * q.n_pairs + s.pair;
+      s.T = f[at + 1] - f[at];
+    } while (s.T == 0);
+    if (s.b != b0) s.L = paged_key_len(q.p, s.b);
+    fill(q);
   }
 };
 
@@ -209,9 +216,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint64_t* o_free = o_fin + 2;       // [2]: the epilogue has read O
   uint64_t* tail = o_free + 2;        // bf16: the V block that holds a sequence's end has landed
   uint64_t* fin = tail + 1;
+  uint64_t* seg_full = fin + 1;       // [SEGS]
+  uint64_t* seg_empty = seg_full + L::SEGS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-  int* first = reinterpret_cast<int*>(smem + L::START_OFF);
+  WideSeg* segs = reinterpret_cast<WideSeg*>(smem + L::SEG_OFF);
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -237,6 +246,10 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     mbar_init(tail, 1);
     mbar_init(fin, 1);
+    for (int i = 0; i < L::SEGS; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], L::READERS);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -245,37 +258,32 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tmem_alloc(tmem_slot, L::TMEM_COLS);
     tmem_relinquish();
   }
-  // the plan is a programmatic dependency: everything above overlaps it
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long W = (long long)p.plan[p.B * q.n_pairs] * p.Hkv;
-  const int cta = int(blockIdx.x), sharers = paged_sharers(W, int(gridDim.x));
-  const long long u0 = cta < sharers ? paged_share(W, cta, sharers) : 0, u1 = cta < sharers ? paged_share(W, cta + 1, sharers) : 0;
-  if (warp == 0 && u0 < u1) {
-    const int b = wide_search(p.plan, 0, p.B, q.n_pairs, p.Hkv, u0, lane);
-    const int64_t at = (int64_t)b * q.n_pairs;
-    const int base = p.plan[at], sum = p.plan[at + q.n_pairs] - base;
-    const long long rem = u0 - (long long)base * p.Hkv;
-    const int h = int(rem / sum), v = base + int(rem % sum);
-    const int pair = wide_search(p.plan + at, 0, q.n_pairs, 1, 1, v, lane);
-    if (lane == 0) {
-      first[0] = b;
-      first[1] = h;
-      first[2] = pair;
-      first[3] = v - p.plan[at + pair];
-      first[4] = p.plan[at + pair + 1] - p.plan[at + pair];
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl wc{q.wait_ns, abort_flag};
-  WideWalk s;
-  s.start(q, first, u1 - u0);
+  const int cta = int(blockIdx.x);
+
+  // Segments come from warp 11 by a ring; every other warp reads them in order.
+  int seg_at = 0;
+  auto next_seg = [&](WideSeg& s) -> bool {
+    const int slot = seg_at % L::SEGS;
+    if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[slot], (seg_at / L::SEGS) & 1, wc))) return false;
+    const volatile int* from = reinterpret_cast<const volatile int*>(&segs[slot]);
+    int* to = reinterpret_cast<int*>(&s);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(WideSeg) / 4); ++i) to[i] = from[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[slot]);
+    ++seg_at;
+    return s.cnt > 0;
+  };
+  WideSeg s;
 
   // Pages of 128 keys from block t on: lane i looks at piece i (a page, or half of a 256-key page).
   const int piece_rows = min(1 << p.page_shift, 128), pieces = 128 / piece_rows;
-  auto piece_page = [&](const WideWalk& w, int j, int i) -> int {   // its page, n_pages (zeros) if bad, -1 past the end
+  auto piece_page = [&](const WideSeg& w, int j, int i) -> int {   // its page, n_pages (zeros) if bad, -1 past the end
     const int key = (w.t + j) * 128 + i * piece_rows;
     if (i >= pieces || key >= w.L) return -1;
     const int id = __ldg(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift));
@@ -288,24 +296,55 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   if (warp >= 8 && warp < 12) {
     set_regs_dec<L::IO_REGS>();
-    if (warp == 11 && !FP8) {
-      // =========================================================== producer of the Q tiles
+    if (warp == 11) {
+      // =========================================================== scheduler, and (bf16) producer of the Q tiles
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan; everything above overlaps it
+      const long long W = (long long)p.plan[p.B * q.n_pairs] * p.Hkv;
+      const int sharers = paged_sharers(W, int(gridDim.x));
+      WideWalk walk{};
+      if (cta < sharers) {
+        const long long u0 = paged_share(W, cta, sharers);
+        walk.left = int(paged_share(W, cta + 1, sharers) - u0);
+        const int b = wide_search(p.plan, 0, p.B, q.n_pairs, p.Hkv, u0, lane);
+        const int64_t at = (int64_t)b * q.n_pairs;
+        const int base = p.plan[at], sum = p.plan[at + q.n_pairs] - base;
+        const long long rem = u0 - (long long)base * p.Hkv;
+        const int h = int(rem / sum), v = base + int(rem % sum);
+        const int pair = wide_search(p.plan + at, 0, q.n_pairs, 1, 1, v, lane);
+        walk.s.b = b;
+        walk.s.h = h;
+        walk.s.pair = pair;
+        walk.s.t = v - p.plan[at + pair];
+        walk.s.T = p.plan[at + pair + 1] - p.plan[at + pair];
+        walk.s.L = paged_key_len(p, b);
+        walk.s.n = paged_new_len(p, b);
+        walk.s.first = 1;
+        walk.fill(q);
+      }
       if (lane == 0) {
-        prefetch_tmap(&tm_q);
+        if constexpr (!FP8) prefetch_tmap(&tm_q);
         int nq[2] = {0, 0};   // Q tiles delivered, per tile
         bool ok = true;
-        for (; ok && s.left > 0; s.next(q)) {
+        for (int i = 0; ok; ++i) {
+          const int slot = i % L::SEGS;
+          if (i >= L::SEGS && !mbar_wait(&seg_empty[slot], ((i / L::SEGS) - 1) & 1, wc)) break;
+          segs[slot] = walk.s;
+          mbar_arrive(&seg_full[slot]);
+          if (walk.s.cnt == 0) break;
+          if constexpr (!FP8) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (s.blocks(q, x) == 0) continue;
-            if (nq[x] >= 1 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc)) { ok = false; break; }
-            mbar_arrive_expect_tx(&q_full[x], D * 2 * q.g * q.tq);
+            for (int x = 0; x < 2; ++x) {
+              if (walk.s.blocks[x] == 0) continue;
+              if (nq[x] >= 1 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc)) { ok = false; break; }
+              mbar_arrive_expect_tx(&q_full[x], D * 2 * q.g * q.tq);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(smem + (x ? L::QB_OFF : L::QA_OFF) + c * L::SUB, &tm_q, &q_full[x], c * 64, 0,
-                          (2 * s.pair + x) * q.tq, s.b * p.Hkv + s.h);
-            ++nq[x];
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(smem + (x ? L::QB_OFF : L::QA_OFF) + c * L::SUB, &tm_q, &q_full[x], c * 64, 0,
+                            (2 * walk.s.pair + x) * q.tq, walk.s.b * p.Hkv + walk.s.h);
+              ++nq[x];
+            }
           }
+          if (ok) walk.next(q);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -323,8 +362,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (lane == 0) prefetch_tmap(map);
       int g = 0, tails = 0;   // blocks delivered so far; those with a sequence's end
       bool ok = true;
-      for (; ok && s.left > 0; s.next(q)) {
-        const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+      while (ok && next_seg(s)) {
+        const int n_max = s.cnt;
         for (int j = 0; j < n_max; ++j, ++g) {
           const int st = g % NS;
           const int page = piece_page(s, j, lane);
@@ -367,8 +406,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       int g = 0;
       bool ok = true;
-      for (; ok && s.left > 0; s.next(q)) {
-        const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+      while (ok && next_seg(s)) {
+        const int n_max = s.cnt;
         for (int j = 0; ok && j < n_max; ++j) {
           const int page = piece_page(s, j, lane);
           const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
@@ -399,10 +438,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       int nb[2] = {0, 0};        // blocks of each tile so far: phase of p_full
       int ni[2] = {0, 0};        // segments with work for each tile so far: phase of q_full, o_free
       bool ok = true;
-      for (; ok && s.left > 0; s.next(q)) {
-        const int n_x[2] = {s.blocks(q, 0), s.blocks(q, 1)};
-        const int n_max = max(n_x[0], n_x[1]);
-        if (n_max == 0) continue;
+      while (ok && next_seg(s)) {
+        const int n_x[2] = {s.blocks[0], s.blocks[1]}, n_max = s.cnt;
         auto issue_s = [&](int x, int kst) {   // S_x = Q_x K^T
           const uint32_t q_lo = s0 + uint32_t((x ? L::QB_OFF : L::QA_OFF) >> 4) + kKM;
           const uint32_t k_lo = s0 + uint32_t((L::K_OFF + kst * L::TILE) >> 4) + kKM;
@@ -484,11 +521,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     int g = 0, gb = 0;        // raw tiles, blocks so far
     int nq[2] = {0, 0};
     bool ok = true;
-    for (; ok && s.left > 0; s.next(q)) {
-      const int n_max = max(s.blocks(q, 0), s.blocks(q, 1));
+    while (ok && next_seg(s)) {
+      const int n_max = s.cnt;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
-        if (s.blocks(q, x) == 0) continue;
+        if (s.blocks[x] == 0) continue;
         if (!__all_sync(0xffffffffu, nq[x] < 1 || mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc))) { ok = false; break; }
         const int i = (2 * s.pair + x) * q.tq + ct / q.g, jj = ct % q.g;
         const bool real = ct < q.g * q.tq && i < p.Nq;
@@ -586,9 +623,9 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t o_addr = lane_base + L::o_col(x);
     const int ii = r / q.g, jj = r % q.g;
     int nb = 0, ni = 0, gb = 0;   // blocks and segments of this tile, blocks of the CTA so far
-    bool ok = true, first_seg = true;
-    for (; ok && s.left > 0; s.next(q), first_seg = false) {
-      const int n = s.blocks(q, x);
+    bool ok = true;
+    while (ok && next_seg(s)) {
+      const int n = s.blocks[x];
       const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
       const bool stored = ii < q.tq && qi < p.Nq;
       const int lim = stored && qi < s.n ? (p.causal ? max(s.L - s.n + qi + 1, 0) : s.L) : 0;   // keys < lim allowed
@@ -697,16 +734,16 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         l = l * alpha + (rs0 + rs1);
       }
       if (!ok) break;
-      gb += max(s.blocks(q, 0), s.blocks(q, 1));
+      gb += s.cnt;
 
       // ---- epilogue: O / l in bf16 and lse, or the segment's partial
       const bool whole = s.t == 0 && s.cnt == s.T;
       const int64_t out = ((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + qi;
-      const int64_t slot = (2 * (int64_t)cta + (first_seg ? 0 : 1)) * 256 + 128 * x + r;
+      const int64_t slot = (2 * (int64_t)cta + (s.first ? 0 : 1)) * 256 + 128 * x + r;
       if (tid == 0) {
         int2* info = p.info + (s.b * p.Hkv + s.h) * q.n_pairs + s.pair;
         if (s.t + s.cnt == s.T) info->y = whole ? -1 : cta;
-        if (s.t == 0) info->x = 2 * cta + (first_seg ? 0 : 1);
+        if (s.t == 0) info->x = 2 * cta + (s.first ? 0 : 1);
       }
       if (lim == 0 || n == 0) l = 0.f;
       if (n > 0) {
@@ -762,6 +799,30 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+// Merges the pairs that several CTAs shared and writes the rows of pairs without keys; a quarter of a pair per
+// CTA, a row per warp at a time.
+template <int D>
+__global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const WideParams q) {
+  const PagedParams& p = q.p;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned item = blockIdx.x / 4;
+  const unsigned bh = item / q.n_pairs, pair = item % q.n_pairs, b = bh / p.Hkv;
+  const int64_t at = (int64_t)b * q.n_pairs + pair;
+  const bool has = p.plan[at + 1] > p.plan[at];
+  const int2 info = p.info[item];
+  if (has && info.y < 0) return;
+  const int rows = q.g * q.tq;   // of a tile
+  for (int k = (blockIdx.x & 3) * 8 + warp; k < 2 * rows; k += 32) {
+    const int x = k >= rows ? 1 : 0, r = k - x * rows;
+    const int i = (2 * pair + x) * q.tq + r / q.g;
+    if (i >= p.Nq) break;
+    PagedMerge<D / 32> a;
+    if (has) a.gather(p, info, 0, 1, 256, 128 * x + r, lane);
+    a.store(p, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, lane);
   }
 }
 
