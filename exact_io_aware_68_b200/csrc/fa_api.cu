@@ -546,8 +546,8 @@ fa_status launch_paged(fa::WideParams q, int sms, cudaStream_t s) {
 }
 
 // Pool of pages as {d, page_size, Hkv, n_pages}, loaded page by page (at most 128 rows): 64 features with the
-// 128-byte swizzle in bf16, whole rows unswizzled in e4m3.
-fa_status make_pool_map(CUtensorMap* map, const void* ptr, bool fp8, int d, int page_size, int Hkv, int n_pages,
+// 128-byte swizzle in bf16; in e4m3 whole rows, K swizzled by their length for the MMA, V not (it is converted).
+fa_status make_pool_map(CUtensorMap* map, const void* ptr, bool fp8, bool is_k, int d, int page_size, int Hkv, int n_pages,
                         int64_t page_bytes, const char* name) {
   auto fn = encode_fn();
   if (fn == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
@@ -558,8 +558,8 @@ fa_status make_pool_map(CUtensorMap* map, const void* ptr, bool fp8, int d, int 
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        fp8 && !is_k ? CU_TENSOR_MAP_SWIZZLE_NONE : fp8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, int(r));
   return FA_OK;
 }
@@ -586,8 +586,8 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   fa_status st;
   const fa::PagedParams& p = q.p;
   if ((st = make_group_map(&mq, p.q, D, q.g, p.Nq, p.B * p.Hkv, q.tq)) != FA_OK) return st;
-  if ((st = make_pool_map(&mk, p.k, FP8, D, page_size, p.Hkv, p.n_pages, p.k_page_bytes, "k_cache")) != FA_OK) return st;
-  if ((st = make_pool_map(&mv, p.v, FP8, D, page_size, p.Hkv, p.n_pages, p.v_page_bytes, "v_cache")) != FA_OK) return st;
+  if ((st = make_pool_map(&mk, p.k, FP8, true, D, page_size, p.Hkv, p.n_pages, p.k_page_bytes, "k_cache")) != FA_OK) return st;
+  if ((st = make_pool_map(&mv, p.v, FP8, false, D, page_size, p.Hkv, p.n_pages, p.v_page_bytes, "v_cache")) != FA_OK) return st;
   auto kernel = fa::fa_paged_wide_kernel<D, FP8>;
   if ((st = set_smem(kernel, L::BYTES)) != FA_OK) return st;
   if ((st = check_launch_regs(kernel, L::LAUNCH_REGS, "fa_fwd_paged wide kernel")) != FA_OK) return st;

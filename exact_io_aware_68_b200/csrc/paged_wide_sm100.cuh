@@ -12,9 +12,10 @@
 //    contiguous share of all units.  A pair that several CTAs share is merged from fp32 partials.
 //  * Pages.  One TMA box per page and 64-feature panel; a 128-key block is 128 / page of them.  Keys past the
 //    sequence's end are not loaded, and their rows of V are zeroed in shared memory (0 * stale would not be 0).
-//  * e4m3.  Four more warps turn the raw tiles into f16 (exact; NaN stays NaN), in the swizzled layout the MMA reads,
-//    and the queries too (each row times a power of two).  The page's key scale multiplies the finished scores, its
-//    value scale the probabilities.
+//  * e4m3.  K enters the tensor core as it is: each query row, times a power of two, is split into an e4m3 and an
+//    e5m2 part (8 bits fit into 4 + 3, see below), and S is the sum of two 8-bit products.  P needs 16 bits, so V
+//    is turned into f16 (exact; NaN stays NaN) by four more warps, in the swizzled layout the MMA reads.  The
+//    page's key scale multiplies the finished scores, its value scale the probabilities.
 #pragma once
 #include "fwd_sm100.cuh"
 #include "paged_sm100.cuh"
@@ -41,23 +42,24 @@ template <int D, bool FP8>
 struct WideLayout {
   static constexpr int TILE = 128 * D * 2;         // bytes of one 128-row 16-bit tile
   static constexpr int SUB = 128 * 128;            // one 64-column swizzle panel of a tile
-  static constexpr int RAW = 128 * D;              // bytes of one 128-row e4m3 tile
-  static constexpr int KST = FP8 ? 2 : (D == 128) ? 3 : 4;
-  static constexpr int VST = (D == 128 || FP8) ? 2 : 4;
-  static constexpr int RST = FP8 ? (D == 128 ? 2 : 4) : 0;   // raw tiles: K_0, V_0, K_1, ...
+  static constexpr int RAW = 128 * D;              // bytes of one 128-row 8-bit tile
+  static constexpr int KTILE = FP8 ? RAW : TILE;
+  static constexpr int KST = FP8 ? 4 : (D == 128) ? 3 : 4;
+  static constexpr int VST = (D == 128) ? 2 : 4;
+  static constexpr int RST = FP8 ? (D == 128 ? 2 : 4) : 0;   // raw V tiles
   static constexpr int SST = 4;                    // scale sets (one per block)
-  static constexpr int QA_OFF = 0;
+  static constexpr int QA_OFF = 0;                 // (e4m3: each query tile is two 8-bit tiles)
   static constexpr int QB_OFF = QA_OFF + TILE;
   static constexpr int K_OFF = QB_OFF + TILE;
-  static constexpr int V_OFF = K_OFF + KST * TILE;
+  static constexpr int V_OFF = K_OFF + KST * KTILE;
   static constexpr int RAW_OFF = V_OFF + VST * TILE;
   static constexpr int SC_OFF = RAW_OFF + RST * RAW;            // [SST][2][8] fp32: K and V scales of the 16-key groups
   static constexpr int QS_OFF = SC_OFF + (FP8 ? SST * 64 : 0);  // [2][2][128] fp32: score scale of the rows, by item parity
   static constexpr int BAR_OFF = QS_OFF + (FP8 ? 2 * 2 * 128 * 4 : 0);
   // q_full[2], q_empty[2], k_full, k_empty, v_full, v_empty, raw_full, raw_empty, s_full[2], p_full[2][2], o_fin[2],
-  // o_free[2], tail, fin, seg_full, seg_empty
+  // o_free[2], tail, fin, seg_full, seg_empty, sc_full
   static constexpr int SEGS = 4;                   // segments scheduled ahead
-  static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2 + 2 * SEGS;
+  static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2 + 2 * SEGS + (FP8 ? SST : 0);
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SEG_OFF = MISC_OFF + 16;
   static constexpr int BYTES = SEG_OFF + SEGS * int(sizeof(WideSeg));
@@ -66,7 +68,7 @@ struct WideLayout {
   static constexpr int TMEM_COLS = 512;
   // Registers per thread of the warpgroups: softmax (2), producers and MMA issuer, converters.
   static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int READERS = FP8 ? 14 : 11;   // warps that read the segments: all but the scheduling one and idle ones
+  static constexpr int READERS = FP8 ? 15 : 11;   // warps that read the segments: all but the scheduling one
   static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
   static constexpr int SOFT_REGS = FP8 ? 176 : 200, IO_REGS = FP8 ? 80 : 104, CVT_REGS = 80;
   static_assert(BYTES <= 232448, "shared memory budget");
@@ -77,6 +79,29 @@ template <int N>
 __device__ __forceinline__ void set_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" :: "n"(N) : "memory"); }
 template <int N>
 __device__ __forceinline__ void set_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" :: "n"(N) : "memory"); }
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit floating point operands, fp32 accumulate; the form of
+// mma_ss_elect.
+__device__ __forceinline__ void mma_ss_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|l, 0xffffffff;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Two fp32 as a pair of e4m3 or e5m2 codes (lo in bits 0-7): nearest, saturating, NaN to NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_e5m2x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 
 // 4-D tiled load (no multicast) into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
@@ -218,6 +243,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint64_t* fin = tail + 1;
   uint64_t* seg_full = fin + 1;       // [SEGS]
   uint64_t* seg_empty = seg_full + L::SEGS;
+  uint64_t* sc_full = seg_empty + L::SEGS;   // [SST]: e4m3: a block's scales are there
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
   WideSeg* segs = reinterpret_cast<WideSeg*>(smem + L::SEG_OFF);
@@ -233,13 +259,15 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&o_free[x], 4);
     }
     for (int s = 0; s < KST; ++s) {
-      mbar_init(&k_full[s], FP8 ? 4 : 1);
+      mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < VST; ++s) {
       mbar_init(&v_full[s], FP8 ? 4 : 1);
       mbar_init(&v_empty[s], 1);
     }
+    if constexpr (FP8)
+      for (int s = 0; s < L::SST; ++s) mbar_init(&sc_full[s], 1);
     for (int s = 0; s < L::RST; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
@@ -351,16 +379,16 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (nq[x] >= 1) mbar_drain(&q_full[x], (nq[x] - 1) & 1, q.wait_ns);
       }
       __syncwarp();
-    } else if (!FP8 && (warp == 8 || warp == 10)) {
-      // =========================================================== producers of the K (warp 8) and V (warp 10) rings
+    } else if (warp == 8 || warp == 10) {
+      // =========================================================== producers of the K (warp 8) and V (warp 10; e4m3: raw V) rings
       const bool is_k = (warp == 8);
-      const int NS = is_k ? KST : VST;
-      uint64_t* full = is_k ? k_full : v_full;
-      uint64_t* empty = is_k ? k_empty : v_empty;
+      const int NS = is_k ? KST : FP8 ? RST : VST;
+      uint64_t* full = is_k ? k_full : FP8 ? raw_full : v_full;
+      uint64_t* empty = is_k ? k_empty : FP8 ? raw_empty : v_empty;
       const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-      uint8_t* ring = smem + (is_k ? L::K_OFF : L::V_OFF);
+      uint8_t* ring = smem + (is_k ? L::K_OFF : FP8 ? L::RAW_OFF : L::V_OFF);
       if (lane == 0) prefetch_tmap(map);
-      int g = 0, tails = 0;   // blocks delivered so far; those with a sequence's end
+      int g = 0, tails = 0;   // blocks delivered so far; those of V in bf16 with a sequence's end
       bool ok = true;
       while (ok && next_seg(s)) {
         const int n_max = s.cnt;
@@ -369,16 +397,20 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const int page = piece_page(s, j, lane);
           const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
           const int key0 = (s.t + j) * 128;
-          const bool ends = !is_k && key0 + 128 > s.L;
+          const bool ends = !FP8 && !is_k && key0 + 128 > s.L;
           if (!__all_sync(0xffffffffu, g < NS || mbar_wait(&empty[st], ((g / NS) - 1) & 1, wc))) { ok = false; break; }
           uint64_t* bar = ends ? tail : &full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * piece_rows * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * piece_rows * (FP8 ? D : 2 * D));
           __syncwarp();
           if (page >= 0) {
             const int y = (key0 + lane * piece_rows) & ((1 << p.page_shift) - 1);
+            if constexpr (FP8) {
+              tma_load_4d(ring + st * L::RAW + lane * piece_rows * D, map, bar, 0, y, s.h, page);
+            } else {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(ring + st * L::TILE + c * L::SUB + lane * piece_rows * 128, map, bar, c * 64, y, s.h, page);
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(ring + st * L::TILE + c * L::SUB + lane * piece_rows * 128, map, bar, c * 64, y, s.h, page);
+            }
           }
           if (ends) {   // rows past the end: zeros, before the block is handed on
             if (!__all_sync(0xffffffffu, mbar_wait(tail, tails & 1, wc))) { ok = false; break; }
@@ -394,42 +426,14 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
       }
       if (lane == 0) {   // every copy started here lands before the CTA releases its shared memory
-        if (!ok && !is_k) mbar_drain(tail, tails & 1, q.wait_ns);   // a copy of an unfinished tail block, if any
+        if (!FP8 && !ok && !is_k) mbar_drain(tail, tails & 1, q.wait_ns);   // a copy of an unfinished tail block, if any
         for (int j = max(0, g - NS); j < g; ++j) mbar_drain(&full[j % NS], (j / NS) & 1, q.wait_ns);
       }
-      __syncwarp();
-    } else if (FP8 && warp == 8) {
-      // =========================================================== producer of the raw tiles
-      if (lane == 0) {
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-      }
-      int g = 0;
-      bool ok = true;
-      while (ok && next_seg(s)) {
-        const int n_max = s.cnt;
-        for (int j = 0; ok && j < n_max; ++j) {
-          const int page = piece_page(s, j, lane);
-          const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
-          const int y = ((s.t + j) * 128 + lane * piece_rows) & ((1 << p.page_shift) - 1);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++g) {
-            const int st = g % RST;
-            if (!__all_sync(0xffffffffu, g < RST || mbar_wait(&raw_empty[st], ((g / RST) - 1) & 1, wc))) { ok = false; break; }
-            if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], __popc(have) * piece_rows * D);
-            __syncwarp();
-            if (page >= 0)
-              tma_load_4d(smem + L::RAW_OFF + st * L::RAW + lane * piece_rows * D, kv ? &tm_v : &tm_k, &raw_full[st], 0, y, s.h, page);
-          }
-        }
-      }
-      if (lane == 0)
-        for (int j = max(0, g - RST); j < g; ++j) mbar_drain(&raw_full[j % RST], (j / RST) & 1, q.wait_ns);
       __syncwarp();
     } else if (warp == 9) {
       // =========================================================== MMA issuer (whole warp, elect.sync)
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
-      constexpr uint32_t kType = FP8 ? (1u << 7) | (1u << 10) : 0u;   // e4m3: f16 operands (format 0) instead of bf16 (1)
+      constexpr uint32_t kType = FP8 ? (1u << 7) | (1u << 10) : 0u;   // e4m3 (S) or f16 (PV) operands, format 0, instead of bf16 (1)
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false) & ~kType;   // Q: K-major, K: K-major
       constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true) & ~kType;     // P: TMEM, V: MN-major
       const uint32_t s0 = smem_u32(smem) >> 4;
@@ -442,11 +446,22 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int n_x[2] = {s.blocks[0], s.blocks[1]}, n_max = s.cnt;
         auto issue_s = [&](int x, int kst) {   // S_x = Q_x K^T
           const uint32_t q_lo = s0 + uint32_t((x ? L::QB_OFF : L::QA_OFF) >> 4) + kKM;
-          const uint32_t k_lo = s0 + uint32_t((L::K_OFF + kst * L::TILE) >> 4) + kKM;
+          const uint32_t k_lo = s0 + uint32_t((L::K_OFF + kst * L::KTILE) >> 4) + kKM;
+          if constexpr (FP8) {
+            // rows of D bytes: the 128-byte swizzle at D = 128, the 64-byte swizzle (layout 4, 8 rows 512 bytes apart) at 64
+            constexpr uint32_t kHi8 = D == 128 ? sdesc_sw128_hi(1024) : ((512u >> 4) | (1u << 14) | (4u << 29));
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * L::SUB + (kk & 3) * 32) >> 4;
-            mma_ss_elect(tmem + L::s_col(x), sdesc_join(q_lo + off, kHi), sdesc_join(k_lo + off, kHi), kIdS, kk > 0 ? 1u : 0u);
+            for (int part = 0; part < 2; ++part)   // the queries' e4m3, then their e5m2 part
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_ss_f8_elect(tmem + L::s_col(x), sdesc_join(q_lo + ((part * L::RAW + kk * 32) >> 4), kHi8),
+                                sdesc_join(k_lo + ((kk * 32) >> 4), kHi8), kIdS | (part ? 1u << 7 : 0u), part + kk > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * L::SUB + (kk & 3) * 32) >> 4;
+              mma_ss_elect(tmem + L::s_col(x), sdesc_join(q_lo + off, kHi), sdesc_join(k_lo + off, kHi), kIdS, kk > 0 ? 1u : 0u);
+            }
           }
         };
         auto issue_pv_half = [&](int x, int vst, int h, uint32_t acc0) {   // O_x += P_x[keys of half h] V[same keys]
@@ -513,12 +528,12 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       __syncwarp();
     }
   } else if (FP8 && warp >= 12) {
-    // =========================================================== converters: e4m3 -> f16, queries bf16 -> f16
+    // =========================================================== converters: V to f16, queries to two 8-bit parts
     set_regs_dec<L::CVT_REGS>();
     const int ct = tid - 384;
     float* scales = reinterpret_cast<float*>(smem + L::SC_OFF);
     float* qscale = reinterpret_cast<float*>(smem + L::QS_OFF);
-    int g = 0, gb = 0;        // raw tiles, blocks so far
+    int gb = 0;        // blocks so far
     int nq[2] = {0, 0};
     bool ok = true;
     while (ok && next_seg(s)) {
@@ -538,20 +553,37 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
         }
-        // each row times a power of two that puts its largest element into [2^14, 2^15)
+        // Each row times a power of two that puts its largest element into [2^7, 2^8).  An element's 8 significant bits
+        // are hi = the nearest e4m3 number and at most 8 units of its last bit, which is 3 significant bits: e5m2.
+        // Elements below 2^-9 (2^-17 of the largest) lose bits: at most 2^-14, that is 2^-21 of the largest element.
         const int ex = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
         const bool scaled = mx > 0.f && mx < INFINITY;
-        const float up = scaled ? __uint_as_float(uint32_t(127 + 14 - ex) << 23) : 1.f;
-        qscale[((nq[x] & 1) * 2 + x) * 128 + ct] = p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 14 + ex) << 23) : 1.f);
-        uint8_t* dst = smem + (x ? L::QB_OFF : L::QA_OFF) + ct * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[4];
+        const float up = scaled ? __uint_as_float(uint32_t(127 + 7 - ex) << 23) : 1.f;
+        qscale[((nq[x] & 1) * 2 + x) * 128 + ct] = p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 7 + ex) << 23) : 1.f);
+        uint8_t* dst = smem + (x ? L::QB_OFF : L::QA_OFF);
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * L::SUB + (((c & 7) ^ (ct & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int y = 0; y < 2; ++y) {
+            const uint4 w = real ? src[2 * c + y] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a = __uint_as_float(u[e] << 16) * up, b = __uint_as_float(u[e] & 0xffff0000u) * up;
+              if (!(fabsf(a) < INFINITY)) a = NAN;   // such a row's scores are NaN (inf - inf) in any case
+              if (!(fabsf(b) < INFINITY)) b = NAN;
+              const uint32_t h2 = pack_e4m3x2(a, b), f2 = e4m3x2_to_f16x2(h2);
+              const uint32_t l2 = pack_e5m2x2(a - __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu))),
+                                              b - __half2float(__ushort_as_half((unsigned short)(f2 >> 16))));
+              const int k = 2 * y + (e >> 1);
+              hi[k] = (e & 1) ? hi[k] | (h2 << 16) : h2;
+              lo[k] = (e & 1) ? lo[k] | (l2 << 16) : l2;
+            }
+          }
+          uint8_t* d = dst + PagedLayout<D, true, 1>::at(ct, c);   // the swizzle of a row of D bytes
+          *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(d + L::RAW) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -559,9 +591,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         ++nq[x];
       }
       if (!ok) break;
-      for (int j = 0; ok && j < n_max; ++j, ++gb) {
+      for (int j = 0; j < n_max; ++j, ++gb) {
         const int key0 = (s.t + j) * 128;
-        float my_scale = 0.f;   // threads 0-15: K and V scale of 16-key group ct & 7
+        const int st = gb % RST, dst_st = gb % VST;
+        // threads 0-15: K and V scale of 16-key group ct & 7 (past the end 1 and 0: its scores are masked)
+        float my_scale = ct < 8 ? 1.f : 0.f;
         if (ct < 16) {
           const int key = key0 + 16 * (ct & 7);
           if (key < s.L) {
@@ -569,47 +603,48 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (unsigned(id) < unsigned(p.n_pages)) my_scale = __ldg((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
           }
         }
+        if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (gb / RST) & 1, wc))) { ok = false; break; }
+        constexpr int CPR = D / 16;   // raw 16-byte chunks per key, and chunks per thread
+        const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
+        uint4 w[CPR];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++g) {
-          const int st = g % RST, NS = kv ? VST : KST, dst_st = gb % NS;
-          uint64_t* empty = kv ? &v_empty[dst_st] : &k_empty[dst_st];
-          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (g / RST) & 1, wc))) { ok = false; break; }
-          if (!__all_sync(0xffffffffu, gb < NS || mbar_wait(empty, ((gb / NS) - 1) & 1, wc))) { ok = false; break; }
-          if (kv == 0 && ct < 16) scales[(gb % L::SST) * 16 + ct] = my_scale;
-          const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
-          uint8_t* dst = smem + (kv ? L::V_OFF : L::K_OFF) + dst_st * L::TILE;
-          constexpr int CPR = D / 16;   // raw 16-byte chunks per key
-#pragma unroll 4
-          for (int i = 0; i < CPR; ++i) {
-            const int id = i * 128 + ct, row = id / CPR, c = id % CPR;
-            const uint4 w = *reinterpret_cast<const uint4*>(raw + id * 16);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[2 * e] = e4m3x2_to_f16x2(u[e]);
-              o[2 * e + 1] = e4m3x2_to_f16x2(u[e] >> 16);
-            }
-            if (key0 + row >= s.L) {   // past the end: what lies there is nobody's
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = 0u;
-            }
-            uint8_t* d = dst + (c >> 2) * L::SUB + row * 128;
-            // 16-bit chunks 2c and 2c + 1 of the row; lanes of the second panel store them in the other order, so
-            // that 8 lanes meet 8 different banks
-            const int z = c >> 2;
-            const int ca = ((2 * c + z) & 7) ^ (row & 7), cb = ((2 * c + 1 - z) & 7) ^ (row & 7);
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(d + (ca << 4)) = z ? hi : lo;
-            *reinterpret_cast<uint4*>(d + (cb << 4)) = z ? lo : hi;
-          }
-          fence_proxy_async_smem();
+        for (int i = 0; i < CPR; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (i * 128 + ct) * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[st]);
+        // (a free stage also means that block gb - VST is done with: its scales, SST blocks back, too)
+        if (!__all_sync(0xffffffffu, gb < VST || mbar_wait(&v_empty[dst_st], ((gb / VST) - 1) & 1, wc))) { ok = false; break; }
+        if (warp == 12) {
+          if (ct < 16) scales[(gb % L::SST) * 16 + ct] = my_scale;
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[st]);
-            mbar_arrive(kv ? &v_full[dst_st] : &k_full[dst_st]);
-          }
+          if (lane == 0) mbar_arrive(&sc_full[gb % L::SST]);
         }
+        uint8_t* dst = smem + L::V_OFF + dst_st * L::TILE;
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+          const int id = i * 128 + ct, row = id / CPR, c = id % CPR;
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * e] = e4m3x2_to_f16x2(u[e]);
+            o[2 * e + 1] = e4m3x2_to_f16x2(u[e] >> 16);
+          }
+          if (key0 + row >= s.L) {   // past the end: what lies there is nobody's
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0u;
+          }
+          uint8_t* d = dst + (c >> 2) * L::SUB + row * 128;
+          // 16-bit chunks 2c and 2c + 1 of the row; lanes of the second panel store them in the other order, so
+          // that 8 lanes meet 8 different banks
+          const int z = c >> 2;
+          const int ca = ((2 * c + z) & 7) ^ (row & 7), cb = ((2 * c + 1 - z) & 7) ^ (row & 7);
+          const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(d + (ca << 4)) = z ? second : first;
+          *reinterpret_cast<uint4*>(d + (cb << 4)) = z ? first : second;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[dst_st]);
       }
     }
   } else {
@@ -645,30 +680,6 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < 4; ++h) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * h]));
-        const volatile float* sc = reinterpret_cast<const volatile float*>(smem + L::SC_OFF) + ((gb + j) % L::SST) * 16;
-        float vmove = 1.f, unit = 1.f;
-        if constexpr (FP8) {
-          if (j == 0) sl2 = reinterpret_cast<const volatile float*>(smem + L::QS_OFF)[((ni & 1) * 2 + x) * 128 + r];
-          float vmax = vref;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float ks = sc[u];
-            vmax = fmaxf(vmax, sc[8 + u]);
-#pragma unroll
-            for (int c = 16 * u; c < 16 * u + 16; c += 2) {
-              float a, b;
-              f2_split(f2_mul(f2_make(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2_make(ks, ks)), a, b);
-              sr[c] = __float_as_uint(a);
-              sr[c + 1] = __float_as_uint(b);
-            }
-          }
-          if (vmax > vref) {
-            vmove = vref / vmax;
-            vref = vmax;
-          }
-          unit = kPagedPScale / vref;
-        }
-
         const int k0 = (s.t + j) * 128;
         if (k0 + 128 > min(lim_lo, s.L)) {   // block straddles a mask edge
           const int keep = lim - k0;         // columns < keep are kept
@@ -676,12 +687,43 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int c = 0; c < 128; ++c)
             if (c >= keep) sr[c] = __float_as_uint(-INFINITY);
         }
-        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent chains
+        // the block's scales: K's of 8 groups of 16 keys, then V's
+        const volatile float* sc = reinterpret_cast<const volatile float*>(smem + L::SC_OFF) + ((gb + j) % L::SST) * 16;
+        float vmove = 1.f, unit = 1.f, kf[8], m_cand;
+        if constexpr (FP8) {
+          // the scores are sr times the group's key scale: it enters the maximum here and the exponent's factor below
+          if (j == 0) sl2 = reinterpret_cast<const volatile float*>(smem + L::QS_OFF)[((ni & 1) * 2 + x) * 128 + r];
+          const int b = gb + j;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[b % L::SST], (b / L::SST) & 1, wc))) { ok = false; break; }
+          float vmax = vref;
+          m_cand = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8)
+          for (int u = 0; u < 8; ++u) {
+            kf[u] = sc[u];
+            vmax = fmaxf(vmax, sc[8 + u]);
+            float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mxv[u] = max3f(mxv[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
-        const float m_cand = fmaxf(max3f(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
+            for (int c = 16 * u; c < 16 * u + 16; c += 4) {
+              m0 = max3f(m0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+              m1 = max3f(m1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+            }
+            m_cand = fmaxf(m_cand, fmaxf(m0, m1) * kf[u]);
+            kf[u] *= sl2;
+          }
+          m_cand *= sl2;
+          if (vmax > vref) {
+            vmove = vref / vmax;
+            vref = vmax;
+          }
+          unit = kPagedPScale / vref;
+        } else {
+          float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent chains
+#pragma unroll
+          for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mxv[u] = max3f(mxv[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
+          m_cand = fmaxf(max3f(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
+        }
         float alpha = 1.f;
         if (m_cand > m_ref + kPagedRescale) {
           alpha = ex2_approx(m_ref - m_cand);
@@ -698,7 +740,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int c = 32 * h + e;   // pair index: keys 2c, 2c + 1
-            uint64_t pp = exp2_pair(sr[2 * c], sr[2 * c + 1], sl2x2, negm2);
+            const uint64_t pp = exp2_pair(sr[2 * c], sr[2 * c + 1], FP8 ? f2_make(kf[c >> 3], kf[c >> 3]) : sl2x2, negm2);
             rs2 = f2_add(rs2, pp);
             float p0, p1;
             if constexpr (FP8) {

@@ -85,6 +85,8 @@ def attention_bounds(q, cache, lens, news, scale, causal, R):
     * a probability is then off by e_s + 2^-21 (ex2.approx, its argument's rounding) relative, and enters the
       matrix product in 16 bits: by half a step of bf16, 2^-8 of it, for more than 8 rows per K/V head; in
       two bf16 parts, 2^-16, for up to 8 rows; in f16 times its page's scale, 2^-11 + 2^-23, with e4m3;
+    * e4m3 with more than 16 rows: a query's elements below 2^-17 of its largest one are off by up to 2^-21 of
+      that one, so a score is off by at most 2^-21 max |q| sum |k| scale more;
     * fp32 sums over L keys add at most L 2^-24; O is rounded to bf16: half a step, 2^-8 |O|.
     So |dO| <= 2^-8 |O| + (2 e_p + c + 2 L 2^-24) sum P |V|, |dlse| <= e_p + L 2^-24 + 2^-21 + |lse| 2^-22."""
     absq, kval, vval = np.abs(q), np.abs(cache.val["k"]), np.abs(cache.val["v"])
@@ -98,6 +100,8 @@ def attention_bounds(q, cache, lens, news, scale, causal, R):
         if L:
             keys = np.repeat(oracle.paged.sequence_keys(kval, cache.table.numpy(), b, L), g, 0)
             kmax[b] = np.einsum("hid,hjd->hij", absq[b], keys).max(-1) * scale
+            if cache.fp8 and R > 16:
+                kmax[b] += 2.0 ** -21 * absq[b].max(-1) * keys.sum(-1).max(-1)[:, None] * scale / ((d + 4) * 2.0 ** -24)
     e_p = (d + 4) * 2.0 ** -24 * kmax + 2.0 ** -21
     L = np.array(lens).reshape(-1, 1, 1) * 2.0 ** -24
     finite = np.where(np.isfinite(lse), lse, 0.0)
