@@ -34,7 +34,7 @@ struct WideParams {
 struct WideSeg {
   int b, h, pair, t, T;   // t: its first block, T: blocks of the pair
   int L, n, cnt;          // keys and new tokens of the sequence, blocks of the segment (0: the share is done)
-  int blocks[2];          // blocks of either tile in it; their maximum is cnt
+  int blocks[2];          // blocks of either tile in it
   int first, pad;         // the CTA's first segment
 };
 
@@ -70,7 +70,7 @@ struct WideLayout {
   static constexpr int THREADS = FP8 ? 512 : 384;
   static constexpr int READERS = FP8 ? 15 : 11;   // warps that read the segments: all but the scheduling one
   static constexpr int LAUNCH_REGS = FP8 ? 128 : 168;
-  static constexpr int SOFT_REGS = FP8 ? 176 : 200, IO_REGS = FP8 ? 80 : 104, CVT_REGS = 80;
+  static constexpr int SOFT_REGS = FP8 ? 152 : 200, IO_REGS = FP8 ? 88 : 104, CVT_REGS = 120;
   static_assert(BYTES <= 232448, "shared memory budget");
   static_assert(2 * SOFT_REGS + IO_REGS + (FP8 ? CVT_REGS : 0) <= THREADS / 128 * LAUNCH_REGS, "register budget");
 };
@@ -295,30 +295,36 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   // Segments come from warp 11 by a ring; every other warp reads them in order.
   int seg_at = 0;
-  auto next_seg = [&](WideSeg& s) -> bool {
-    const int slot = seg_at % L::SEGS;
-    if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[slot], (seg_at / L::SEGS) & 1, wc))) return false;
-    const volatile int* from = reinterpret_cast<const volatile int*>(&segs[slot]);
+  auto read_seg = [&]() {
+    WideSeg s;
+    const volatile int* from = reinterpret_cast<const volatile int*>(&segs[seg_at % L::SEGS]);
     int* to = reinterpret_cast<int*>(&s);
 #pragma unroll
     for (int i = 0; i < int(sizeof(WideSeg) / 4); ++i) to[i] = from[i];
+    return s;
+  };
+  auto wait_seg = [&]() {
+    return __all_sync(0xffffffffu, mbar_wait(&seg_full[seg_at % L::SEGS], (seg_at / L::SEGS) & 1, wc));
+  };
+  auto release_seg = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&seg_empty[slot]);
+    if (lane == 0) mbar_arrive(&seg_empty[seg_at % L::SEGS]);
     ++seg_at;
+  };
+  auto next_seg = [&](WideSeg& s) -> bool {
+    if (!wait_seg()) return false;
+    s = read_seg();
+    release_seg();
     return s.cnt > 0;
   };
   WideSeg s;
 
   // Pages of 128 keys from block t on: lane i looks at piece i (a page, or half of a 256-key page).
   const int piece_rows = min(1 << p.page_shift, 128), pieces = 128 / piece_rows;
-  auto piece_page = [&](const WideSeg& w, int j, int i) -> int {   // its page, n_pages (zeros) if bad, -1 past the end
+  auto has_piece = [&](const WideSeg& w, int j, int i) { return i < pieces && (w.t + j) * 128 + i * piece_rows < w.L; };
+  auto piece_page = [&](const WideSeg& w, int j, int i) -> int {   // its page (not looked at yet)
     const int key = (w.t + j) * 128 + i * piece_rows;
-    if (i >= pieces || key >= w.L) return -1;
-    const int id = __ldg(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift));
-    if (unsigned(id) >= unsigned(p.n_pages)) {
-      record_status(kStatusRange);
-      return p.n_pages;
-    }
+    const int id = has_piece(w, j, i) ? __ldg(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift)) : 0;
     return id;
   };
 
@@ -392,24 +398,32 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       bool ok = true;
       while (ok && next_seg(s)) {
         const int n_max = s.cnt;
+        int next_page = piece_page(s, 0, lane);
         for (int j = 0; j < n_max; ++j, ++g) {
           const int st = g % NS;
-          const int page = piece_page(s, j, lane);
-          const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+          const int page = next_page;
+          if (j + 1 < n_max) next_page = piece_page(s, j + 1, lane);   // in flight during the wait below
+          const bool mine = has_piece(s, j, lane);
+          const unsigned have = __ballot_sync(0xffffffffu, mine);
           const int key0 = (s.t + j) * 128;
           const bool ends = !FP8 && !is_k && key0 + 128 > s.L;
           if (!__all_sync(0xffffffffu, g < NS || mbar_wait(&empty[st], ((g / NS) - 1) & 1, wc))) { ok = false; break; }
           uint64_t* bar = ends ? tail : &full[st];
           if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * piece_rows * (FP8 ? D : 2 * D));
           __syncwarp();
-          if (page >= 0) {
+          if (mine) {
+            int from = page;
+            if (unsigned(page) >= unsigned(p.n_pages)) {   // outside the pool: the copy fills in zeros
+              record_status(kStatusRange);
+              from = p.n_pages;
+            }
             const int y = (key0 + lane * piece_rows) & ((1 << p.page_shift) - 1);
             if constexpr (FP8) {
-              tma_load_4d(ring + st * L::RAW + lane * piece_rows * D, map, bar, 0, y, s.h, page);
+              tma_load_4d(ring + st * L::RAW + lane * piece_rows * D, map, bar, 0, y, s.h, from);
             } else {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(ring + st * L::TILE + c * L::SUB + lane * piece_rows * 128, map, bar, c * 64, y, s.h, page);
+                tma_load_4d(ring + st * L::TILE + c * L::SUB + lane * piece_rows * 128, map, bar, c * 64, y, s.h, from);
             }
           }
           if (ends) {   // rows past the end: zeros, before the block is handed on
@@ -591,18 +605,24 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         ++nq[x];
       }
       if (!ok) break;
+      // threads 0-15: K and V scale of 16-key group ct & 7 (past the end 1 and 0: its scores are masked), looked up
+      // one block ahead, its page two blocks
+      auto group_page = [&](int j) -> int {
+        const int key = (s.t + j) * 128 + 16 * (ct & 7);
+        return ct < 16 && j < n_max && key < s.L ? __ldg(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
+      };
+      auto group_scale = [&](int id) -> float {
+        if (unsigned(id) >= unsigned(p.n_pages)) return ct < 8 ? 1.f : 0.f;
+        return __ldg((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
+      };
+      float next_scale = group_scale(group_page(0));
+      int next_id = group_page(1);
       for (int j = 0; j < n_max; ++j, ++gb) {
         const int key0 = (s.t + j) * 128;
         const int st = gb % RST, dst_st = gb % VST;
-        // threads 0-15: K and V scale of 16-key group ct & 7 (past the end 1 and 0: its scores are masked)
-        float my_scale = ct < 8 ? 1.f : 0.f;
-        if (ct < 16) {
-          const int key = key0 + 16 * (ct & 7);
-          if (key < s.L) {
-            const int id = __ldg(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift));
-            if (unsigned(id) < unsigned(p.n_pages)) my_scale = __ldg((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
-          }
-        }
+        const float my_scale = next_scale;
+        next_scale = group_scale(next_id);
+        next_id = group_page(j + 2);
         if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (gb / RST) & 1, wc))) { ok = false; break; }
         constexpr int CPR = D / 16;   // raw 16-byte chunks per key, and chunks per thread
         const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
@@ -659,12 +679,20 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int ii = r / q.g, jj = r % q.g;
     int nb = 0, ni = 0, gb = 0;   // blocks and segments of this tile, blocks of the CTA so far
     bool ok = true;
-    while (ok && next_seg(s)) {
-      const int n = s.blocks[x];
-      const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
-      const bool stored = ii < q.tq && qi < p.Nq;
-      const int lim = stored && qi < s.n ? (p.causal ? max(s.L - s.n + qi + 1, 0) : s.L) : 0;   // keys < lim allowed
-      const int lim_lo = p.causal ? s.L - s.n + i0 + 1 : s.L;                                // the tile's smallest
+    while (ok && wait_seg()) {
+      // What the block loop needs of the segment; the rest is read again at its end (registers are short here, and
+      // with shared memory taking nearly all of L1 a spilled one is a trip to L2).
+      int n, key0, lim, lim_lo;
+      {
+        const WideSeg s = read_seg();
+        if (s.cnt == 0) break;
+        n = s.blocks[x];
+        key0 = s.t * 128;
+        const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
+        const bool stored = ii < q.tq && qi < p.Nq;
+        lim = stored && qi < s.n ? (p.causal ? max(s.L - s.n + qi + 1, 0) : s.L) : 0;   // keys < lim allowed
+        lim_lo = min(p.causal ? s.L - s.n + i0 + 1 : s.L, s.L);                        // the tile's smallest
+      }
       float sl2 = p.scale_log2;
       float m_ref = -INFINITY;   // reference max, exp2 domain
       float l = 0.f;
@@ -672,90 +700,36 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int j = 0; j < n; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], (nb + j) & 1, wc))) { ok = false; break; }
         tc_fence_after();
-        uint32_t sr[128];
-        tmem_ld32(s_addr + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_ld32(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-        tmem_ld32(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
-        tmem_ld_wait();
+        const int k0 = key0 + j * 128;
+        if (k0 + 128 > lim_lo) {   // block straddles a mask edge: its scores are masked in place, 32 columns at a time
+          const int keep = lim - k0;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t m[32];
+            tmem_ld32(s_addr + c0, m);
+            tmem_ld_wait();
+            reg_fence32(m);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[32 * h]));
-        const int k0 = (s.t + j) * 128;
-        if (k0 + 128 > min(lim_lo, s.L)) {   // block straddles a mask edge
-          const int keep = lim - k0;         // columns < keep are kept
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= keep) sr[c] = __float_as_uint(-INFINITY);
-        }
-        // the block's scales: K's of 8 groups of 16 keys, then V's
-        const volatile float* sc = reinterpret_cast<const volatile float*>(smem + L::SC_OFF) + ((gb + j) % L::SST) * 16;
-        float vmove = 1.f, unit = 1.f, kf[8], m_cand;
-        if constexpr (FP8) {
-          // the scores are sr times the group's key scale: it enters the maximum here and the exponent's factor below
-          if (j == 0) sl2 = reinterpret_cast<const volatile float*>(smem + L::QS_OFF)[((ni & 1) * 2 + x) * 128 + r];
-          const int b = gb + j;
-          if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[b % L::SST], (b / L::SST) & 1, wc))) { ok = false; break; }
-          float vmax = vref;
-          m_cand = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            kf[u] = sc[u];
-            vmax = fmaxf(vmax, sc[8 + u]);
-            float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-            for (int c = 16 * u; c < 16 * u + 16; c += 4) {
-              m0 = max3f(m0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-              m1 = max3f(m1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-            }
-            m_cand = fmaxf(m_cand, fmaxf(m0, m1) * kf[u]);
-            kf[u] *= sl2;
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c >= keep) m[c] = __float_as_uint(-INFINITY);
+            tmem_st32(s_addr + c0, m);
           }
-          m_cand *= sl2;
-          if (vmax > vref) {
-            vmove = vref / vmax;
-            vref = vmax;
-          }
-          unit = kPagedPScale / vref;
-        } else {
-          float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent chains
-#pragma unroll
-          for (int c = 0; c < 128; c += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mxv[u] = max3f(mxv[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
-          m_cand = fmaxf(max3f(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
+          tmem_st_wait();
         }
-        float alpha = 1.f;
-        if (m_cand > m_ref + kPagedRescale) {
-          alpha = ex2_approx(m_ref - m_cand);
-          m_ref = m_cand;
-        }
-        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const uint64_t sl2x2 = f2_make(sl2, sl2), negm2 = f2_make(-m_use, -m_use);
+        float alpha = 1.f, o_move;
         uint64_t rs2 = f2_make(0.f, 0.f);
-        const float o_move = alpha * vmove;
-        float vs = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // two halves of 64 keys; the MMA takes each half as soon as it is ready
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int c = 32 * h + e;   // pair index: keys 2c, 2c + 1
-            const uint64_t pp = exp2_pair(sr[2 * c], sr[2 * c + 1], FP8 ? f2_make(kf[c >> 3], kf[c >> 3]) : sl2x2, negm2);
-            rs2 = f2_add(rs2, pp);
-            float p0, p1;
-            if constexpr (FP8) {
-              if ((e & 7) == 0) vs = sc[8 + (c >> 3)] * unit;   // 8 pairs: one 16-key group
-              f2_split(f2_mul(pp, f2_make(vs, vs)), p0, p1);
-              pk[e] = pack_f16x2(p0, p1);
-            } else {
-              f2_split(pp, p0, p1);
-              pk[e] = pack_bf16x2(p0, p1);
-            }
+        auto move_max = [&](float m_cand) {
+          if (m_cand > m_ref + kPagedRescale) {
+            alpha = ex2_approx(m_ref - m_cand);
+            m_ref = m_cand;
           }
-          // P over the score columns already read; O already holds PV up to block j-1
+          return m_ref == -INFINITY ? 0.f : -m_ref;
+        };
+        // P of half h over score columns already read; O already holds PV up to block j - 1
+        auto hand_over = [&](int h, const uint32_t (&pk)[32]) {
           tmem_st32(s_addr + 32 * h, pk);
           if (h == 0 && j >= 1 && __any_sync(0xffffffffu, o_move != 1.f)) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t orr[32];
               tmem_ld32(o_addr + c * 32, orr);
@@ -770,15 +744,111 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
+        };
+        if constexpr (FP8) {
+          // The scores are read twice, 64 at a time (registers and instruction cache are short here).  sc: K's scales
+          // of the block's 8 groups of 16 keys, then V's.
+          if (j == 0) sl2 = *reinterpret_cast<const volatile float*>(smem + L::QS_OFF + (((ni & 1) * 2 + x) * 128 + r) * 4);
+          const int b = gb + j;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[b % L::SST], (b / L::SST) & 1, wc))) { ok = false; break; }
+          const uint32_t sc = smem_u32(smem) + L::SC_OFF + (b % L::SST) * 64;
+          auto scales4 = [&](int at, float (&f)[4]) {
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(sc + 4 * at));
+          };
+          auto load64 = [&](int h, uint32_t (&sr)[64]) {
+            tmem_ld32(s_addr + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            tmem_ld32(s_addr + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            tmem_ld_wait();
+            reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          };
+          float vmax = vref, m_cand = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sr[64];
+            float ks[4], vs[4];
+            scales4(4 * h, ks);
+            scales4(8 + 4 * h, vs);
+            load64(h, sr);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              vmax = fmaxf(vmax, vs[u]);
+              float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+              for (int c = 16 * u; c < 16 * u + 16; c += 4) {
+                m0 = max3f(m0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                m1 = max3f(m1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+              }
+              m_cand = fmaxf(m_cand, fmaxf(m0, m1) * ks[u]);   // the scores are sr times the group's key scale
+            }
+          }
+          const float neg = move_max(m_cand * sl2);
+          const uint64_t negm2 = f2_make(neg, neg);
+          o_move = alpha;
+          if (vmax > vref) {
+            o_move *= vref / vmax;
+            vref = vmax;
+          }
+          const float unit = kPagedPScale / vref;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {   // the MMA takes each half as soon as it is ready
+            uint32_t sr[64], pk[32];
+            float ks[4], vs[4];
+            scales4(4 * h, ks);
+            scales4(8 + 4 * h, vs);
+            load64(h, sr);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float kf = ks[e >> 3] * sl2, vf = vs[e >> 3] * unit;   // 8 pairs: one group
+              const uint64_t pp = exp2_pair(sr[2 * e], sr[2 * e + 1], f2_make(kf, kf), negm2);
+              rs2 = f2_add(rs2, pp);
+              float p0, p1;
+              f2_split(f2_mul(pp, f2_make(vf, vf)), p0, p1);
+              pk[e] = pack_f16x2(p0, p1);
+            }
+            hand_over(h, pk);
+          }
+        } else {
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_ld32(s_addr + c, *reinterpret_cast<uint32_t(*)[32]>(&sr[c]));
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[c]));
+          float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent chains
+#pragma unroll
+          for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mxv[u] = max3f(mxv[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
+          const float neg = move_max(fmaxf(max3f(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2);
+          const uint64_t sl2x2 = f2_make(sl2, sl2), negm2 = f2_make(neg, neg);
+          o_move = alpha;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint64_t pp = exp2_pair(sr[64 * h + 2 * e], sr[64 * h + 2 * e + 1], sl2x2, negm2);
+              rs2 = f2_add(rs2, pp);
+              float p0, p1;
+              f2_split(pp, p0, p1);
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            hand_over(h, pk);
+          }
         }
         float rs0, rs1;
         f2_split(rs2, rs0, rs1);
         l = l * alpha + (rs0 + rs1);
       }
       if (!ok) break;
-      gb += s.cnt;
 
       // ---- epilogue: O / l in bf16 and lse, or the segment's partial
+      const WideSeg s = read_seg();
+      release_seg();
+      gb += s.cnt;
+      const int qi = (2 * s.pair + x) * q.tq + ii;
+      const bool stored = ii < q.tq && qi < p.Nq;
       const bool whole = s.t == 0 && s.cnt == s.T;
       const int64_t out = ((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + qi;
       const int64_t slot = (2 * (int64_t)cta + (s.first ? 0 : 1)) * 256 + 128 * x + r;
