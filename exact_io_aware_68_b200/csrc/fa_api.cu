@@ -483,9 +483,9 @@ PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int64_t max_keys) {
 int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
 constexpr int kPagedMostWarps = 16;
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-// The workspace: partial O, partial (m, l), plan, info.
+// The workspace: partial O, partial (m, l), plan, info, redo.
 struct PagedSpace {
-  size_t ml, plan, info, total;   // byte offsets
+  size_t ml, plan, info, redo, total;   // byte offsets
 };
 PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
   const size_t rows = size_t(paged_ctas(sms)) * (s.wide ? 1 : kPagedMostWarps) * 2 * s.rows;
@@ -493,7 +493,8 @@ PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
   w.ml = up256(rows * d * 4);
   w.plan = w.ml + up256(rows * 8);
   w.info = w.plan + up256(size_t(s.plan) * 4);
-  w.total = w.info + up256(size_t(B) * Hkv * s.tiles * 8);
+  w.redo = w.info + up256(size_t(B) * Hkv * s.tiles * 8);
+  w.total = w.redo + (s.wide ? up256(size_t(B) * Hkv * s.tiles * 4) : 0);
   return w;
 }
 
@@ -665,6 +666,7 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   q4.g = Hq / Hkv;
   q4.tq = shape.tq;
   q4.n_pairs = shape.tiles;
+  q4.redo = reinterpret_cast<int*>(ws + space.redo);
   q4.wait_ns = g_wait_ns.load();
   if (shape.wide) {
     if (d == 64) return fp8 ? launch_paged_wide<64, true>(q4, page_size, sms, s) : launch_paged_wide<64, false>(q4, page_size, sms, s);

@@ -27,6 +27,7 @@ struct WideParams {
   int g;          // query heads per K/V head, <= 128
   int tq;         // positions per tile: floor(128 / g)
   int n_pairs;    // tile pairs per (sequence, K/V head)
+  int* redo;      // [B, Hkv, n_pairs]: nonzero where the merge has to compute the pair anew
   uint64_t wait_ns;
 };
 
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const WideParams q)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int total = q.p.B * q.n_pairs;
   if (tid == 0) carry = q.p.plan[0] = 0;
+  for (int i = tid; i < total * q.p.Hkv; i += 1024) q.redo[i] = 0;
   __syncthreads();
   for (int base = 0; base < total; base += 1024) {
     const int at = base + tid;
@@ -862,6 +864,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!__all_sync(0xffffffffu, mbar_wait(&o_fin[x], ni & 1, wc))) { ok = false; break; }
         tc_fence_after();
       }
+      float zero = 0.f;   // stays 0 unless O has a value that is not finite
       const float f = l != 0.f ? (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? 1.f / l : 1.f) : 0.f;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -872,6 +875,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           reg_fence32(orr);
         }
         if (!stored) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) zero = fmaf(__uint_as_float(orr[e]), 0.f, zero);
         if (whole) {
           uint32_t w[16];
 #pragma unroll
@@ -889,6 +894,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                          orr[e + 6], orr[e + 7]);
         }
       }
+      // 0 * inf: a value behind a row's causal mask may have reached it
+      if (p.causal && stored && l != 0.f && n > 0 && !(zero == 0.f)) q.redo[(s.b * p.Hkv + s.h) * q.n_pairs + s.pair] = 1;
       if (n > 0) {   // O has been read: the next segment's first PV may overwrite it
         tc_fence_before();
         __syncwarp();
@@ -914,6 +921,51 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
+// One query row by one warp, key by key: for pairs whose O is not finite.  There a value of V that is not
+// finite lies within the tiles, and the tensor core adds 0 * V = NaN to rows that do not see its key; here a row reads what
+// it sees and nothing else.  Rare, so only its result counts.
+template <int D>
+__device__ __noinline__ void paged_row(const PagedParams& p, int b, int h, int64_t row, int lim, int lane) {
+  constexpr int PER = D / 32;
+  const bool fp8 = p.k_scale != nullptr;
+  float q[PER], acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    q[e] = __bfloat162float(p.q[row * D + lane * PER + e]);
+    acc[e] = 0.f;
+  }
+  auto value = [&](const uint8_t* pool, int64_t at) {   // element `at` of a pool
+    if (!fp8) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[at]);
+    return __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(pool[at]) & 0xffffu)));
+  };
+  float m = -INFINITY, l = 0.f;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int j = 0; j < lim; ++j) {
+      const int id = p.page_table[(int64_t)b * p.max_pages + (j >> p.page_shift)];
+      if (unsigned(id) >= unsigned(p.n_pages)) continue;   // (already reported)
+      const int64_t in = (((int64_t)h << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + lane * PER;
+      const uint8_t *k = p.k + id * p.k_page_bytes, *v = p.v + id * p.v_page_bytes;
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) s = fmaf(q[e], value(k, in + e), s);
+#pragma unroll
+      for (int z = 16; z > 0; z >>= 1) s += __shfl_xor_sync(0xffffffffu, s, z);
+      s *= p.scale_log2 * (fp8 ? p.k_scale[(int64_t)id * p.Hkv + h] : 1.f);
+      if (pass == 0) {
+        m = fmaxf(m, s);
+        continue;
+      }
+      const float w = exp2f(s - m);
+      l += w;
+      const float vs = fp8 ? p.v_scale[(int64_t)id * p.Hkv + h] : 1.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, value(v, in + e) * vs, acc[e]);
+    }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) p.o[row * D + lane * PER + e] = __float2bfloat16_rn(l != 0.f ? acc[e] / l : 0.f);
+  if (lane == 0) p.lse[row] = l != 0.f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+}
+
 // Merges the pairs that several CTAs shared and writes the rows of pairs without keys; a quarter of a pair per
 // CTA, a row per warp at a time.
 template <int D>
@@ -926,12 +978,18 @@ __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const WidePa
   const int64_t at = (int64_t)b * q.n_pairs + pair;
   const bool has = p.plan[at + 1] > p.plan[at];
   const int2 info = p.info[item];
-  if (has && info.y < 0) return;
+  const bool redo = has && q.redo[item] != 0;
+  if (has && info.y < 0 && !redo) return;
   const int rows = q.g * q.tq;   // of a tile
   for (int k = (blockIdx.x & 3) * 8 + warp; k < 2 * rows; k += 32) {
     const int x = k >= rows ? 1 : 0, r = k - x * rows;
     const int i = (2 * pair + x) * q.tq + r / q.g;
     if (i >= p.Nq) break;
+    if (redo) {
+      const int L = paged_key_len(p, b), n = paged_new_len(p, b);   // (set only under a causal mask)
+      paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, i < n ? max(L - n + i + 1, 0) : 0, lane);
+      continue;
+    }
     PagedMerge<D / 32> a;
     if (has) a.gather(p, info, 0, 1, 256, 128 * x + r, lane);
     a.store(p, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, lane);
