@@ -597,9 +597,12 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
       kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mk, mv, q);
   if (st != FA_OK) return st;
-  // B Hkv pairs < 2^29: B Hq Nq < 2^31 and a pair has at least g positions' rows
-  return launch_dependent<fa::WideParams>(fa::fa_paged_wide_combine_kernel<D>, unsigned(p.B) * p.Hkv * q.n_pairs * 4, 256, 0, s,
-                                          "fa_fwd_paged combine kernel launch", q);
+  // pairs < 2^27: B Hq Nq < 2^31, and all but the last pair of a head have more than 126 rows
+  const unsigned pairs = unsigned(p.B) * p.Hkv * q.n_pairs;
+  st = launch_dependent<fa::WideParams>(fa::fa_paged_wide_combine_kernel<D>, pairs * fa::kWideMergeCtas, 256, 0, s,
+                                        "fa_fwd_paged combine kernel launch", q);
+  if (st != FA_OK || !p.causal || p.Nq == 1) return st;
+  return launch_dependent<fa::WideParams>(fa::fa_paged_wide_redo_kernel<D>, pairs, 256, 0, s, "fa_fwd_paged redo kernel launch", q);
 }
 
 fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

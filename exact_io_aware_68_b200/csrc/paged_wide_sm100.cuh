@@ -27,7 +27,7 @@ struct WideParams {
   int g;          // query heads per K/V head, <= 128
   int tq;         // positions per tile: floor(128 / g)
   int n_pairs;    // tile pairs per (sequence, K/V head)
-  int* redo;      // [B, Hkv, n_pairs]: nonzero where the merge has to compute the pair anew
+  int* redo;      // [B, Hkv, n_pairs]: nonzero where the pair has to be computed anew
   uint64_t wait_ns;
 };
 
@@ -925,7 +925,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 // finite lies within the tiles, and the tensor core adds 0 * V = NaN to rows that do not see its key; here a row reads what
 // it sees and nothing else.  Rare, so only its result counts.
 template <int D>
-__device__ __noinline__ void paged_row(const PagedParams& p, int b, int h, int64_t row, int lim, int lane) {
+__device__ __forceinline__ void paged_row(const PagedParams& p, int b, int h, int64_t row, int lim, int lane) {
   constexpr int PER = D / 32;
   const bool fp8 = p.k_scale != nullptr;
   float q[PER], acc[PER];
@@ -966,33 +966,46 @@ __device__ __noinline__ void paged_row(const PagedParams& p, int b, int h, int64
   if (lane == 0) p.lse[row] = l != 0.f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
 }
 
-// Merges the pairs that several CTAs shared and writes the rows of pairs without keys; a quarter of a pair per
-// CTA, a row per warp at a time.
+// Merges the pairs that several CTAs shared and writes the rows of pairs without keys: a row per warp at a time,
+// 2 rows a warp (with 8, four CTAs a pair, latency kept it at 20 us on 256 pairs of 2 partials, 38 MB).
+constexpr int kWideMergeCtas = 16;
 template <int D>
-__global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const WideParams q) {
+__global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid_constant__ WideParams q) {
   const PagedParams& p = q.p;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned item = blockIdx.x / 4;
+  const unsigned item = blockIdx.x / kWideMergeCtas;
   const unsigned bh = item / q.n_pairs, pair = item % q.n_pairs, b = bh / p.Hkv;
   const int64_t at = (int64_t)b * q.n_pairs + pair;
   const bool has = p.plan[at + 1] > p.plan[at];
   const int2 info = p.info[item];
-  const bool redo = has && q.redo[item] != 0;
-  if (has && info.y < 0 && !redo) return;
+  if (has && info.y < 0) return;
   const int rows = q.g * q.tq;   // of a tile
-  for (int k = (blockIdx.x & 3) * 8 + warp; k < 2 * rows; k += 32) {
+  for (int k = (blockIdx.x % kWideMergeCtas) * 8 + warp; k < 2 * rows; k += 8 * kWideMergeCtas) {
     const int x = k >= rows ? 1 : 0, r = k - x * rows;
     const int i = (2 * pair + x) * q.tq + r / q.g;
     if (i >= p.Nq) break;
-    if (redo) {
-      const int L = paged_key_len(p, b), n = paged_new_len(p, b);   // (set only under a causal mask)
-      paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, i < n ? max(L - n + i + 1, 0) : 0, lane);
-      continue;
-    }
     PagedMerge<D / 32> a;
     if (has) a.gather(p, info, 0, 1, 256, 128 * x + r, lane);
     a.store(p, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, lane);
+  }
+}
+
+// The pairs that have to be computed anew; one CTA a pair.  After the merge, and only under a causal mask.
+template <int D>
+__global__ void __launch_bounds__(256) fa_paged_wide_redo_kernel(const __grid_constant__ WideParams q) {
+  const PagedParams& p = q.p;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned item = blockIdx.x;
+  if (q.redo[item] == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = item / q.n_pairs, pair = item % q.n_pairs, b = bh / p.Hkv;
+  const int rows = q.g * q.tq, L = paged_key_len(p, b), n = paged_new_len(p, b);
+  for (int k = warp; k < 2 * rows; k += 8) {
+    const int i = (2 * pair + k / rows) * q.tq + k % rows / q.g;
+    if (i >= p.Nq) break;
+    paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + k % rows % q.g) * p.Nq + i, i < n ? min(max(L - n + i + 1, 0), L) : 0, lane);
   }
 }
 
