@@ -452,8 +452,8 @@ int log2_of(int x) {
 }
 
 // How fa_fwd_paged cuts its rows, by sizes alone (host arithmetic).  R = (Hq / Hkv) Nq query rows share a K/V head:
-//  * up to 16 rows, or what the wide kernel's plan cannot index: tiles of 8 (R <= 8) or 16 consecutive rows,
-//    independent warps (paged_sm100.cuh);
+//  * up to 24 rows (32 at d = 64), or what the wide kernel's plan cannot index: tiles of 8, 16, 24 (32) consecutive
+//    rows, independent warps (paged_sm100.cuh);
 //  * more: pairs of 128-row tiles on the tensor memory path (paged_wide_sm100.cuh).
 struct PagedShape {
   bool wide;
@@ -462,10 +462,10 @@ struct PagedShape {
   int tiles;       // tiles (pairs) per (sequence, K/V head)
   int64_t plan;    // entries of the plan
 };
-PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int64_t max_keys) {
+PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int d, int64_t max_keys) {
   const int g = Hq / Hkv, R = g * Nq;
   PagedShape s{};
-  if (R > 16 && g <= 128) {
+  if (R > (d == 64 ? 32 : 24) && g <= 128) {
     s.tq = 128 / g;
     s.tiles = (Nq + 2 * s.tq - 1) / (2 * s.tq);
     s.rows = 256;
@@ -474,7 +474,7 @@ PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int64_t max_keys) {
     if (s.wide) return s;
   }
   s.wide = false;
-  s.rows = s.tq = R <= 8 ? 8 : 16;
+  s.rows = s.tq = R <= 8 ? 8 : R <= 16 ? 16 : R <= 24 || d == 128 ? 24 : 32;
   s.tiles = (R + s.rows - 1) / s.rows;
   s.plan = B + 1;
   return s;
@@ -605,6 +605,15 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   return launch_dependent<fa::WideParams>(fa::fa_paged_wide_redo_kernel<D>, pairs, 256, 0, s, "fa_fwd_paged redo kernel launch", q);
 }
 
+template <int D>
+fa_status launch_paged_rows(const fa::WideParams& q, bool fp8, int rows, int sms, cudaStream_t s) {
+  if constexpr (D == 64)
+    if (rows == 32) return fp8 ? launch_paged<D, true, 4>(q, sms, s) : launch_paged<D, false, 4>(q, sms, s);
+  if (rows == 24) return fp8 ? launch_paged<D, true, 3>(q, sms, s) : launch_paged<D, false, 3>(q, sms, s);
+  if (rows == 16) return fp8 ? launch_paged<D, true, 2>(q, sms, s) : launch_paged<D, false, 2>(q, sms, s);
+  return fp8 ? launch_paged<D, true, 1>(q, sms, s) : launch_paged<D, false, 1>(q, sms, s);
+}
+
 fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                     const float* v_scale, void* o, float* lse, int64_t k_page_stride, int64_t v_page_stride,
                     const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens, int B, int Hq, int Hkv,
@@ -630,7 +639,7 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(FA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   int sms = 0;
-  const PagedShape shape = paged_shape(B, Hq, Hkv, Nq, int64_t(max_pages) * page_size);
+  const PagedShape shape = paged_shape(B, Hq, Hkv, Nq, d, int64_t(max_pages) * page_size);
   const size_t least = paged_space(B, Hkv, shape, d, 1).total;   // refused without a device too
   if (workspace_bytes < least) return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, needs more than %zu", workspace_bytes, least);
   if ((st = sm_count(&sms)) != FA_OK) return st;
@@ -675,13 +684,7 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
     if (d == 64) return fp8 ? launch_paged_wide<64, true>(q4, page_size, sms, s) : launch_paged_wide<64, false>(q4, page_size, sms, s);
     return fp8 ? launch_paged_wide<128, true>(q4, page_size, sms, s) : launch_paged_wide<128, false>(q4, page_size, sms, s);
   }
-  const bool two = shape.rows == 16;
-  if (d == 64) {
-    if (fp8) return two ? launch_paged<64, true, 2>(q4, sms, s) : launch_paged<64, true, 1>(q4, sms, s);
-    return two ? launch_paged<64, false, 2>(q4, sms, s) : launch_paged<64, false, 1>(q4, sms, s);
-  }
-  if (fp8) return two ? launch_paged<128, true, 2>(q4, sms, s) : launch_paged<128, true, 1>(q4, sms, s);
-  return two ? launch_paged<128, false, 2>(q4, sms, s) : launch_paged<128, false, 1>(q4, sms, s);
+  return d == 64 ? launch_paged_rows<64>(q4, fp8, shape.rows, sms, s) : launch_paged_rows<128>(q4, fp8, shape.rows, sms, s);
 }
 
 fa_status run_append(bool fp8, const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
@@ -1089,8 +1092,8 @@ size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   if (int64_t(B) * Hq * Nq >= (int64_t(1) << 31)) return 0;
   // enough for either way of cutting the rows (which one it is depends on the page table's width too)
   const int sms = decode_sms();
-  const size_t wide = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, 0), d, sms).total;
-  const size_t narrow = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, int64_t(1) << 40), d, sms).total;
+  const size_t wide = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, d, 0), d, sms).total;
+  const size_t narrow = paged_space(B, Hkv, paged_shape(B, Hq, Hkv, Nq, d, int64_t(1) << 40), d, sms).total;
   return wide > narrow ? wide : narrow;
 }
 

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[x][ng][e] = s2[ng][e] = 0.f;
-      constexpr int BATCH = FP8 ? 4 : 8;   // chunk pairs loaded ahead of their MMAs
+      constexpr int BATCH = FP8 || NG > 1 ? 4 : 8;   // chunks loaded ahead of their MMAs
 #pragma unroll
       for (int c0 = 0; c0 < Lt::CPR; c0 += BATCH) {
         uint32_t r[BATCH / 2][4];   // keys 0-7 and 8-15 at chunk c, keys 0-7 and 8-15 at chunk c + 1
