@@ -442,6 +442,8 @@ fa_status check_paged(int B, int Hq, int Hkv, int Nq, int d, int n_pages, int pa
     if (s < page || s % 16 != 0)
       return fail(FA_ERR_INVALID_ARG, "page stride %lld must be a multiple of 16, at least Hkv * page_size * d = %lld",
                   (long long)s, (long long)page);
+  for (const int64_t s : {k_page_stride, v_page_stride})
+    if (s >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "page stride %lld must be below 2^31", (long long)s);
   return FA_OK;
 }
 
@@ -663,8 +665,8 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   p.page_table = page_table;
   p.key_lens = key_lens;
   p.new_lens = new_lens;
-  p.k_page_bytes = k_page_stride * (fp8 ? 1 : 2);
-  p.v_page_bytes = v_page_stride * (fp8 ? 1 : 2);
+  p.k_page_bytes = uint32_t(k_page_stride * (fp8 ? 1 : 2));
+  p.v_page_bytes = uint32_t(v_page_stride * (fp8 ? 1 : 2));
   p.B = B;
   p.Hkv = Hkv;
   p.Nq = Nq;

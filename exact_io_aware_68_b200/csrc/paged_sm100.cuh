@@ -53,7 +53,7 @@ struct PagedParams {
   const int32_t* page_table;   // [B, max_pages]
   const int32_t* key_lens;     // [B]
   const int32_t* new_lens;     // [B] or null
-  int64_t k_page_bytes, v_page_bytes;   // from one page to the next
+  uint32_t k_page_bytes, v_page_bytes;   // from one page to the next
   int B, Hkv, Nq, R, row_tiles;         // R = rows per K/V head
   int n_pages, page_shift, max_pages;
   int n_warps;                 // of the whole grid
@@ -61,8 +61,13 @@ struct PagedParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {   // 16 bytes, zeros if not valid
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+template <int OFF>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {   // 16 bytes from src + OFF
+  asm volatile("cp.async.cg.shared.global [%0], [%1 + %2], 16;" :: "r"(dst), "l"(src), "n"(OFF) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool valid) {   // zeros if not valid
+  asm volatile("cp.async.cg.shared.global [%0], [%1 + %3], 16, %2;" :: "r"(dst), "l"(src), "r"(valid ? 16 : 0), "n"(OFF) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
@@ -89,6 +94,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c = a b
+template <bool F16>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // two e4m3 codes (the low 16 bits of w) as f16x2: exact, NaN stays NaN
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
@@ -159,10 +175,15 @@ struct PagedLayout {
   }
 };
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // Where a warp stands in the list of (sequence, head and row tile, key tile)s.
 struct PagedPos {
-  int b, hr, t;   // sequence, head * row_tiles + row tile, key tile
-  int T, L;       // key tiles and keys of sequence b
+  int b, h, rt, t;   // sequence, K/V head, row tile, key tile
+  int T, L;          // key tiles and keys of sequence b
 };
 
 template <int D, bool FP8, int NG>
@@ -220,16 +241,20 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
     ld.b = lo;
     ld.T = off[lo + 1] - off[lo];
     const long long rem = w0 - (long long)off[lo] * HR;
-    ld.hr = (rem >> 32) ? int(rem / ld.T) : int(unsigned(rem) / unsigned(ld.T));
-    ld.t = int(rem - (long long)ld.hr * ld.T);
+    const int hr = (rem >> 32) ? int(rem / ld.T) : int(unsigned(rem) / unsigned(ld.T));
+    ld.t = int(rem - (long long)hr * ld.T);
+    ld.h = hr / p.row_tiles;
+    ld.rt = hr % p.row_tiles;
     ld.L = paged_key_len(p, lo);
   }
   PagedPos cp = ld;
   auto advance = [&](PagedPos& x) {
     if (++x.t < x.T) return;
     x.t = 0;
-    if (++x.hr < HR) return;
-    x.hr = 0;
+    if (++x.rt < p.row_tiles) return;
+    x.rt = 0;
+    if (++x.h < p.Hkv) return;
+    x.h = 0;
     do ++x.b; while (x.b < p.B && off[x.b + 1] == off[x.b]);
     if (x.b < p.B) {
       x.T = off[x.b + 1] - off[x.b];
@@ -247,31 +272,47 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       ids[x] = key < ld.L ? __ldg(p.page_table + (int64_t)ld.b * p.max_pages + (key >> p.page_shift)) : 0;
     }
   };
+  // A lane copies chunk c of keys r0, r0 + RPI, ... of each group.  RPI is a power of two and r0 below it, so the swizzle
+  // of key i RPI + r0 is that of r0 with the bits of i RPI flipped in.
+  constexpr int RPI = 32 / Lt::CPR;   // keys per warp-wide copy
+  const int c0 = lane % Lt::CPR, r0 = lane / Lt::CPR;
+  const uint32_t lane_at = uint32_t(Lt::at(r0, c0)), lane_from = uint32_t(r0 * Lt::ROWB + c0 * 16);
   auto load = [&](int stage) {
     const uint32_t dst = ring + stage * Lt::STAGE;
-    const int h = ld.hr / p.row_tiles;
-    constexpr int RPI = 32 / Lt::CPR;   // keys per warp-wide copy
-    const int c = lane % Lt::CPR, r0 = lane / Lt::CPR;
 #pragma unroll
     for (int x = 0; x < G; ++x) {
       const int key = ld.t * KT + 16 * x;
       const bool ok = unsigned(ids[x]) < unsigned(p.n_pages);
       if (!ok) record_status(kStatusRange);
-      const int64_t page = ok ? ids[x] : 0;
-      const int64_t in = ((int64_t)h << p.page_shift) + (key & page_mask);
-      const uint8_t* ks = p.k + page * p.k_page_bytes + (in + r0) * Lt::ROWB + c * 16;
-      const uint8_t* vs = p.v + page * p.v_page_bytes + (in + r0) * Lt::ROWB + c * 16;
-      const int left = ok ? ld.L - key - r0 : 0;
-#pragma unroll
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int at = Lt::at(16 * x + i * RPI + r0, c);
-        cp_async16(dst + at, ks + i * RPI * Lt::ROWB, i * RPI < left);
-        cp_async16(dst + Lt::TILE + at, vs + i * RPI * Lt::ROWB, i * RPI < left);
-      }
+      const unsigned page = ok ? ids[x] : 0;
+      const unsigned in = ((unsigned(ld.h) << p.page_shift) + (key & page_mask)) * Lt::ROWB + lane_from;   // within the page
+      const uint8_t* ks = p.k + (uint64_t(page) * p.k_page_bytes + in);
+      const uint8_t* vs = p.v + (uint64_t(page) * p.v_page_bytes + in);
+      const int left = ok ? ld.L - key : 0;
+      auto copy = [&](auto all) {
+        auto one = [&](auto i_) {
+          constexpr int i = decltype(i_)::value;
+          if constexpr (i < 16 / RPI) {
+            constexpr int row = 16 * i * RPI / 16;
+            // (at(r0, c0) has its swizzle in bits 4-6)
+            const uint32_t at = Lt::ROWB == 64 ? lane_at + row * 64 : (lane_at ^ ((row & 7) << 4)) + row * Lt::ROWB;
+            const uint32_t to = dst + 16 * x * Lt::ROWB + at;
+            if constexpr (decltype(all)::value) {
+              cp_async16<row * Lt::ROWB>(to, ks);
+              cp_async16<row * Lt::ROWB>(to + Lt::TILE, vs);
+            } else {
+              cp_async16_if<row * Lt::ROWB>(to, ks, row + r0 < left);
+              cp_async16_if<row * Lt::ROWB>(to + Lt::TILE, vs, row + r0 < left);
+            }
+          }
+        };
+        one(Int<0>()); one(Int<1>()); one(Int<2>()); one(Int<3>()); one(Int<4>()); one(Int<5>()); one(Int<6>()); one(Int<7>());
+      };
+      if (left >= 16) copy(Int<1>()); else copy(Int<0>());   // past the end: zeros
       if constexpr (FP8) {
         if (lane < 2)
-          cp_async4(dst + 2 * Lt::TILE + 8 * x + 4 * lane, (lane == 0 ? p.k_scale : p.v_scale) + page * p.Hkv + h,
-                    ok && key < ld.L);
+          cp_async4(dst + 2 * Lt::TILE + 8 * x + 4 * lane, (lane == 0 ? p.k_scale : p.v_scale) + (uint64_t(page) * p.Hkv + ld.h),
+                    left > 0);
       }
     }
   };
@@ -295,7 +336,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   float o[NG][C][4];
   float m[NG][2], l[NG][2], sc[NG][2];   // rows 2 t4 + i; sc: score scale in the log2 domain
   int lim[NG][2], limg[NG], lim_lo;      // keys < lim allowed; limg: of row g; lim_lo: the smallest that is not zero
-  float vref = 0.f;                      // e4m3: the largest value scale so far, O is in units of it
+  float vref = 0.f, unit = 0.f;          // e4m3: the largest value scale so far, O is in units of it; kPagedPScale / vref
   int stage = 0;
   bool fresh = true;
   long long seg = w0;                    // first tile of the running segment
@@ -304,7 +345,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       // ---- queries and limits of this row tile
       fresh = false;
       seg = w;
-      const int h = cp.hr / p.row_tiles, rt = cp.hr % p.row_tiles;
+      const int h = cp.h, rt = cp.rt;
       const int n = paged_new_len(p, cp.b);
       const __nv_bfloat16* qb = p.q + ((int64_t)(cp.b * p.Hkv + h) * p.R + rt * RT) * D;
       lim_lo = cp.L;
@@ -359,6 +400,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       }
       lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
       vref = 6.0185311e-36f;   // 2^-117
+      unit = kPagedPScale / vref;
     }
 
     // ---- the next tile of the list goes into the stage that the previous iteration emptied
@@ -381,10 +423,6 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
 #pragma unroll
     for (int x = 0; x < G; ++x) {
       float s2[NG][4];
-#pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][ng][e] = s2[ng][e] = 0.f;
       constexpr int BATCH = FP8 || NG > 1 ? 4 : 8;   // chunks loaded ahead of their MMAs
 #pragma unroll
       for (int c0 = 0; c0 < Lt::CPR; c0 += BATCH) {
@@ -399,15 +437,24 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
             for (int z = 0; z < 2; ++z) {
               const uint32_t a0 = e4m3x2_to_f16x2(r[y][2 * z]), a2 = e4m3x2_to_f16x2(r[y][2 * z] >> 16);
               const uint32_t a1 = e4m3x2_to_f16x2(r[y][2 * z + 1]), a3 = e4m3x2_to_f16x2(r[y][2 * z + 1] >> 16);
+              const int c = c0 + 2 * y + z;
 #pragma unroll
-              for (int ng = 0; ng < NG; ++ng)
-                mma16816<true>(z == 0 ? s[x][ng] : s2[ng], a0, a1, a2, a3, qf[ng][c0 + 2 * y + z][0], qf[ng][c0 + 2 * y + z][1]);
+              for (int ng = 0; ng < NG; ++ng) {
+                if (c < 2)
+                  mma16816_first<true>(z == 0 ? s[x][ng] : s2[ng], a0, a1, a2, a3, qf[ng][c][0], qf[ng][c][1]);
+                else
+                  mma16816<true>(z == 0 ? s[x][ng] : s2[ng], a0, a1, a2, a3, qf[ng][c][0], qf[ng][c][1]);
+              }
             }
           } else {
+            const int c = c0 / 2 + y;
 #pragma unroll
-            for (int ng = 0; ng < NG; ++ng)
-              mma16816<false>((y & 1) == 0 ? s[x][ng] : s2[ng], r[y][0], r[y][1], r[y][2], r[y][3], qf[ng][c0 / 2 + y][0],
-                              qf[ng][c0 / 2 + y][1]);
+            for (int ng = 0; ng < NG; ++ng) {
+              if (c < 2)
+                mma16816_first<false>((y & 1) == 0 ? s[x][ng] : s2[ng], r[y][0], r[y][1], r[y][2], r[y][3], qf[ng][c][0], qf[ng][c][1]);
+              else
+                mma16816<false>((y & 1) == 0 ? s[x][ng] : s2[ng], r[y][0], r[y][1], r[y][2], r[y][3], qf[ng][c][0], qf[ng][c][1]);
+            }
           }
         }
       }
@@ -460,9 +507,9 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       if (vmax > vref) {   // the same in every lane
         vmove = vref / vmax;
         vref = vmax;
+        unit = kPagedPScale / vref;
         over = true;
       }
-      const float unit = kPagedPScale / vref;
 #pragma unroll
       for (int x = 0; x < G; ++x) vsc[x] *= unit;
     }
@@ -628,9 +675,9 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
     // ---- end of the segment: this row tile's last key tile, or this warp's last
     if (cp.t + 1 == cp.T || w + 1 == w1) {
       const bool whole = cp.t + 1 == cp.T && w - seg + 1 == cp.T;
-      const int h = cp.hr / p.row_tiles, rt = cp.hr % p.row_tiles;
+      const int h = cp.h, rt = cp.rt;
       if (lane == 0) {
-        int2* info = p.info + cp.b * HR + cp.hr;
+        int2* info = p.info + (cp.b * p.Hkv + h) * p.row_tiles + rt;
         if (cp.t + 1 == cp.T) info->y = whole ? -1 : me;
         if (cp.t - int(w - seg) == 0) info->x = 2 * me + (seg == w0 ? 0 : 1);
       }

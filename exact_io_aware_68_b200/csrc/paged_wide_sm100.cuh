@@ -944,7 +944,7 @@ __device__ __forceinline__ void paged_row(const PagedParams& p, int b, int h, in
       const int id = p.page_table[(int64_t)b * p.max_pages + (j >> p.page_shift)];
       if (unsigned(id) >= unsigned(p.n_pages)) continue;   // (already reported)
       const int64_t in = (((int64_t)h << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + lane * PER;
-      const uint8_t *k = p.k + id * p.k_page_bytes, *v = p.v + id * p.v_page_bytes;
+      const uint8_t *k = p.k + uint64_t(id) * p.k_page_bytes, *v = p.v + uint64_t(id) * p.v_page_bytes;
       float s = 0.f;
 #pragma unroll
       for (int e = 0; e < PER; ++e) s = fmaf(q[e], value(k, in + e), s);
