@@ -191,9 +191,10 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 }
 
 // One CTA of THREADS per (sequence, touched page, head, key or value): its new rows stay in registers
-// (at most 4 per thread) between the search for the scale and the rounding.
+// (at most 4 per thread) between the search for the scale and the rounding, as the bf16 they came in: rotating
+// them twice costs less than the registers of the results.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) fa_kv_append_e4m3_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) fa_kv_append_e4m3_kernel(const AppendParams p) {
   if (int(blockIdx.x) < p.row_blocks) {
     append_rows<false>(p, int(blockIdx.x));
     return;
@@ -216,15 +217,8 @@ __global__ void __launch_bounds__(THREADS) fa_kv_append_e4m3_kernel(const Append
   const long long base = (long long)pg << p.page_shift;
   if (base >= L) return;
   const int lo = int(base > start ? base : start), hi = int(base + page_size < L ? base + page_size : L);
-  const int64_t page = __ldg(p.page_table + (int64_t)b * p.max_pages + pg);
-  if (page < 0 || page >= p.n_pages) {
-    record_status(kStatusRange);
-    return;
-  }
-  float* scale = p.scale[kv] + page * p.Hkv + h;
-  uint8_t* dst = p.pool[kv] + page * p.page_bytes[kv] + ((int64_t)h << p.page_shift) * p.d;
+  const int64_t page = __ldg(p.page_table + (int64_t)b * p.max_pages + pg);   // (in flight with the rows)
   const int old = lo - int(base), m = hi - lo;
-  const float before = old > 0 ? *scale : 0.f;
 
   const int lpr = p.d / 16, lane = int(threadIdx.x) % lpr, r0 = int(threadIdx.x) / lpr, rpp = THREADS / lpr;
   int ca, cb;
@@ -240,22 +234,32 @@ __global__ void __launch_bounds__(THREADS) fa_kv_append_e4m3_kernel(const Append
     wa[u] = __ldg(row + ca);
     wb[u] = __ldg(row + cb);
   }
-  float x[4][8], y[4][8];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = r0 + u * rpp;
-    if (r >= m) continue;
-    unpack8(wa[u], x[u]);
-    unpack8(wb[u], y[u]);
+  if (page < 0 || page >= p.n_pages) {
+    record_status(kStatusRange);
+    return;
+  }
+  float* scale = p.scale[kv] + page * p.Hkv + h;
+  uint8_t* dst = p.pool[kv] + page * p.page_bytes[kv] + ((int64_t)h << p.page_shift) * p.d;
+  const float before = old > 0 ? *scale : 0.f;
+  // row u of this thread, rotated
+  auto row_of = [&](int u, float (&x)[8], float (&y)[8]) {
+    unpack8(wa[u], x);
+    unpack8(wb[u], y);
     if (turned) {
       float c[8], s[8];
-      load8(p.cos + (int64_t)(lo + r) * (p.rot / 2) + 8 * lane, c);
-      load8(p.sin + (int64_t)(lo + r) * (p.rot / 2) + 8 * lane, s);
-      turn16(x[u], y[u], c, s, p.interleaved != 0);
+      load8(p.cos + (int64_t)(lo + r0 + u * rpp) * (p.rot / 2) + 8 * lane, c);
+      load8(p.sin + (int64_t)(lo + r0 + u * rpp) * (p.rot / 2) + 8 * lane, s);
+      turn16(x, y, c, s, p.interleaved != 0);
     }
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (r0 + u * rpp >= m) continue;
+    float x[8], y[8];
+    row_of(u, x, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float ax = fabsf(x[u][e]), ay = fabsf(y[u][e]);
+      const float ax = fabsf(x[e]), ay = fabsf(y[e]);
       if (ax < INFINITY) amax = fmaxf(amax, ax);
       if (ay < INFINITY) amax = fmaxf(amax, ay);
     }
@@ -286,21 +290,36 @@ __global__ void __launch_bounds__(THREADS) fa_kv_append_e4m3_kernel(const Append
       *reinterpret_cast<uint2*>(dst + 8 * c) = pack8_e4m3(z);
     }
   }
-  // x / after: after is a power of two unless the caller's own scale was not
+  // x / after.  after is a power of two, and the product with its inverse exact, unless the caller's own scale was not:
+  // then divide.  (A select between the two pays for both: 64 divisions a thread.)
   const bool pow2 = (__float_as_uint(after) & 0x7fffffu) == 0;
   const float inv = 1.f / after;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int r = r0 + u * rpp;
     if (r >= m) continue;
+    float x[8], y[8];
+    row_of(u, x, y);
+    if (!pow2) {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[u][e] = pow2 ? x[u][e] * inv : __fdiv_rn(x[u][e], after);
-      y[u][e] = pow2 ? y[u][e] * inv : __fdiv_rn(y[u][e], after);
+        for (int z = 0; z < 8; ++z)
+          if (z == e) {
+            x[z] = __fdiv_rn(x[z], after);
+            y[z] = __fdiv_rn(y[z], after);
+          }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= inv;
+        y[e] *= inv;
+      }
     }
     uint8_t* row = dst + (int64_t)(old + r) * p.d;
-    *reinterpret_cast<uint2*>(row + 8 * ca) = pack8_e4m3(x[u]);
-    *reinterpret_cast<uint2*>(row + 8 * cb) = pack8_e4m3(y[u]);
+    *reinterpret_cast<uint2*>(row + 8 * ca) = pack8_e4m3(x);
+    *reinterpret_cast<uint2*>(row + 8 * cb) = pack8_e4m3(y);
   }
   if (threadIdx.x == 0 && after != before) *scale = after;
 }
