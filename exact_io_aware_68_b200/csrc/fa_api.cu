@@ -463,10 +463,12 @@ struct PagedShape {
   int tq;          // rows, or positions, per tile
   int tiles;       // tiles (pairs) per (sequence, K/V head)
   int64_t plan;    // entries of the plan
+  int R;           // rows per K/V head
 };
 PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int d, int64_t max_keys) {
   const int g = Hq / Hkv, R = g * Nq;
   PagedShape s{};
+  s.R = R;
   if (R > (d == 64 ? 32 : 24) && g <= 128) {
     s.tq = 128 / g;
     s.tiles = (Nq + 2 * s.tq - 1) / (2 * s.tq);
@@ -485,9 +487,9 @@ PagedShape paged_shape(int B, int Hq, int Hkv, int Nq, int d, int64_t max_keys) 
 int paged_ctas(int sms) { return sms <= 0 || sms > 512 ? 512 : sms; }
 constexpr int kPagedMostWarps = 16;
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-// The workspace: partial O, partial (m, l), plan, info, redo.
+// The workspace: partial O, partial (m, l), plan, info; wide: redo, and for e4m3 pools the queries in 8 bits, their scales.
 struct PagedSpace {
-  size_t ml, plan, info, redo, total;   // byte offsets
+  size_t ml, plan, info, redo, q8, q_scale, total;   // byte offsets
 };
 PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
   const size_t rows = size_t(paged_ctas(sms)) * (s.wide ? 1 : kPagedMostWarps) * 2 * s.rows;
@@ -496,7 +498,9 @@ PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
   w.plan = w.ml + up256(rows * 8);
   w.info = w.plan + up256(size_t(s.plan) * 4);
   w.redo = w.info + up256(size_t(B) * Hkv * s.tiles * 8);
-  w.total = w.redo + (s.wide ? up256(size_t(B) * Hkv * s.tiles * 4) : 0);
+  w.q8 = w.redo + (s.wide ? up256(size_t(B) * Hkv * s.tiles * 4) : 0);
+  w.q_scale = w.q8 + (s.wide ? up256(size_t(B) * Hkv * s.R * d * 2) : 0);
+  w.total = w.q_scale + (s.wide ? up256(size_t(B) * Hkv * s.R * 4) : 0);
   return w;
 }
 
@@ -566,17 +570,19 @@ fa_status make_pool_map(CUtensorMap* map, const void* ptr, bool fp8, bool is_k, 
   if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, int(r));
   return FA_OK;
 }
-// Queries as {d, heads of a group, Nq, B * Hkv}: a box is 64 features of all the group's heads at tq positions.
-fa_status make_group_map(CUtensorMap* map, const void* ptr, int d, int g, int Nq, int BH, int tq) {
+// Queries as {d, heads of a group, Nq, B * Hkv}: a box is 64 features (8 bits: all of them) of all the group's heads
+// at tq positions.
+fa_status make_group_map(CUtensorMap* map, const void* ptr, bool bits8, int d, int g, int Nq, int BH, int tq) {
   auto fn = encode_fn();
   if (fn == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
-  const cuuint64_t row = cuuint64_t(d) * 2;
+  const cuuint64_t row = cuuint64_t(d) * (bits8 ? 1 : 2);
   const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(g), cuuint64_t(Nq), cuuint64_t(BH)};
   const cuuint64_t strides[3] = {row * Nq, row, row * Nq * g};
-  const cuuint32_t box[4] = {64, cuuint32_t(g), cuuint32_t(tq), 1};
+  const cuuint32_t box[4] = {cuuint32_t(bits8 ? d : 64), cuuint32_t(g), cuuint32_t(tq), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(map, bits8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
+                        dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        bits8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed with CUresult %d", int(r));
   return FA_OK;
@@ -585,19 +591,25 @@ fa_status make_group_map(CUtensorMap* map, const void* ptr, int d, int g, int Nq
 template <int D, bool FP8>
 fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cudaStream_t s) {
   using L = fa::WideLayout<D, FP8>;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mq2, mk, mv;
   fa_status st;
   const fa::PagedParams& p = q.p;
-  if ((st = make_group_map(&mq, p.q, D, q.g, p.Nq, p.B * p.Hkv, q.tq)) != FA_OK) return st;
+  const int64_t rows = int64_t(p.B) * p.Hkv * p.R;
+  const void* q1 = FP8 ? static_cast<const void*>(q.q8) : p.q;
+  const void* q2 = FP8 ? static_cast<const void*>(q.q8 + rows * D) : p.q;   // (bf16: not used)
+  if ((st = make_group_map(&mq, q1, FP8, D, q.g, p.Nq, p.B * p.Hkv, q.tq)) != FA_OK) return st;
+  if ((st = make_group_map(&mq2, q2, FP8, D, q.g, p.Nq, p.B * p.Hkv, q.tq)) != FA_OK) return st;
   if ((st = make_pool_map(&mk, p.k, FP8, true, D, page_size, p.Hkv, p.n_pages, p.k_page_bytes, "k_cache")) != FA_OK) return st;
   if ((st = make_pool_map(&mv, p.v, FP8, false, D, page_size, p.Hkv, p.n_pages, p.v_page_bytes, "v_cache")) != FA_OK) return st;
   auto kernel = fa::fa_paged_wide_kernel<D, FP8>;
   if ((st = set_smem(kernel, L::BYTES)) != FA_OK) return st;
   if ((st = check_launch_regs(kernel, L::LAUNCH_REGS, "fa_fwd_paged wide kernel")) != FA_OK) return st;
-  fa::fa_paged_plan_kernel<<<1, 1024, 0, s>>>(q);
+  // one CTA plans; e4m3: the others, at most two per SM, prepare the queries, D / 8 threads a row
+  const int64_t split = FP8 ? std::min<int64_t>((rows + 8191 / D) / (8192 / D), 2 * sms) : 0;
+  fa::fa_paged_plan_kernel<D, FP8><<<unsigned(1 + split), 1024, 0, s>>>(q);
   if ((st = launch_status("fa_fwd_paged plan kernel launch")) != FA_OK) return st;
-  st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
-      kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mk, mv, q);
+  st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
+      kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mq2, mk, mv, q);
   if (st != FA_OK) return st;
   // pairs < 2^27: B Hq Nq < 2^31, and all but the last pair of a head have more than 126 rows
   const unsigned pairs = unsigned(p.B) * p.Hkv * q.n_pairs;
@@ -681,6 +693,8 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   q4.tq = shape.tq;
   q4.n_pairs = shape.tiles;
   q4.redo = reinterpret_cast<int*>(ws + space.redo);
+  q4.q8 = reinterpret_cast<uint8_t*>(ws + space.q8);
+  q4.q_scale = reinterpret_cast<float*>(ws + space.q_scale);
   q4.wait_ns = g_wait_ns.load();
   if (shape.wide) {
     if (d == 64) return fp8 ? launch_paged_wide<64, true>(q4, page_size, sms, s) : launch_paged_wide<64, false>(q4, page_size, sms, s);

@@ -27,6 +27,8 @@ struct WideParams {
   int g;          // query heads per K/V head, <= 128
   int tq;         // positions per tile: floor(128 / g)
   int n_pairs;    // tile pairs per (sequence, K/V head)
+  uint8_t* q8;    // e4m3: [2][B, Hq, Nq, D]: the queries' e4m3 and e5m2 parts
+  float* q_scale; // [B, Hq, Nq]: what they stand for, times the softmax scale
   int* redo;      // [B, Hkv, n_pairs]: nonzero where the pair has to be computed anew
   uint64_t wait_ns;
 };
@@ -55,8 +57,7 @@ struct WideLayout {
   static constexpr int V_OFF = K_OFF + KST * KTILE;
   static constexpr int RAW_OFF = V_OFF + VST * TILE;
   static constexpr int SC_OFF = RAW_OFF + RST * RAW;            // [SST][2][8] fp32: K and V scales of the 16-key groups
-  static constexpr int QS_OFF = SC_OFF + (FP8 ? SST * 64 : 0);  // [2][2][128] fp32: score scale of the rows, by item parity
-  static constexpr int BAR_OFF = QS_OFF + (FP8 ? 2 * 2 * 128 * 4 : 0);
+  static constexpr int BAR_OFF = SC_OFF + (FP8 ? SST * 64 : 0);
   // q_full[2], q_empty[2], k_full, k_empty, v_full, v_empty, raw_full, raw_empty, s_full[2], p_full[2][2], o_fin[2],
   // o_free[2], tail, fin, seg_full, seg_empty, sc_full
   static constexpr int SEGS = 4;                   // segments scheduled ahead
@@ -92,15 +93,15 @@ __device__ __forceinline__ void mma_ss_f8_elect(uint32_t d_tmem, uint64_t a_desc
       "@l tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Two fp32 as a pair of e4m3 or e5m2 codes (lo in bits 0-7): nearest, saturating, NaN to NaN.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+// f16x2 to a pair of e4m3 or e5m2 codes (bits 0-15): nearest, saturating, NaN to NaN.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
   uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_e5m2x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t x) {
   uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e5m2x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e5m2x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}\n" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -120,9 +121,63 @@ __device__ __forceinline__ int wide_keys(const WideParams& q, int L, int n, int 
   return q.p.causal ? min(max(L - n + min(n, i1), 0), L) : L;
 }
 
-// Prefix of the block counts of all (sequence, tile pair)s, into p.plan.  One CTA.
-__global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const WideParams q) {
+// Queries as two 8-bit parts.  Each row times a power of two that puts its largest element into [2^7, 2^8).  An element's
+// 8 significant bits are hi = the nearest e4m3 number and at most 8 units of its last bit, which is 3 significant bits:
+// e5m2.  Elements below 2^-9 (2^-17 of the largest) lose bits: at most 2^-14, that is 2^-21 of the largest element.
+// A row with an element that is not finite becomes NaN, as its scores are (inf - inf) in any case.  In a kernel
+// of its own since by the warps of the main one it took 4 us a tile at each segment's start (latency, cold code).
+template <int D>
+__device__ __forceinline__ void wide_split_queries(const WideParams& q) {
+  constexpr int LPR = D / 8;   // lanes per row
+  const int64_t rows = (int64_t)q.p.B * q.p.Hkv * q.p.R;
+  const int c = threadIdx.x % LPR;
+  for (int64_t row = ((int64_t)(blockIdx.x - 1) * 1024 + threadIdx.x) / LPR; row < (rows + 31) / 32 * 32; row += (int64_t)(gridDim.x - 1) * (1024 / LPR)) {
+    const bool real = row < rows;
+    const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(q.p.q + row * D) + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float mx = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = fabsf(__uint_as_float(u[e] << 16)), b = fabsf(__uint_as_float(u[e] & 0xffff0000u));
+      mx = max3f(mx, a, b);
+      finite = finite && a < INFINITY && b < INFINITY;
+    }
+#pragma unroll
+    for (int z = 1; z < LPR; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+    const unsigned all = __ballot_sync(0xffffffffu, finite);
+    const unsigned mine = (LPR == 16 ? 0xffffu : 0xffu) << (threadIdx.x % 32 / LPR * LPR);
+    const int ex = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
+    const bool scaled = mx > 0.f;
+    const float up = (all & mine) != mine ? NAN : scaled ? __uint_as_float(uint32_t(127 + 7 - ex) << 23) : 1.f;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);   // exact down to 2^-17
+      const uint32_t h2 = f16x2_to_e4m3x2(x), f2 = e4m3x2_to_f16x2(h2);
+      uint32_t rest;   // x - hi
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(x), "r"(f2));
+      const uint32_t l2 = f16x2_to_e5m2x2(rest);
+      hi[e >> 1] = (e & 1) ? hi[e >> 1] | (h2 << 16) : h2;
+      lo[e >> 1] = (e & 1) ? lo[e >> 1] | (l2 << 16) : l2;
+    }
+    if (!real) continue;
+    *reinterpret_cast<uint2*>(q.q8 + row * D + 8 * c) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(q.q8 + (rows + row) * D + 8 * c) = make_uint2(lo[0], lo[1]);
+    if (c == 0) q.q_scale[row] = q.p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 7 + ex) << 23) : 1.f);
+  }
+}
+
+// Prefix of the block counts of all (sequence, tile pair)s, into p.plan, by the first CTA; with e4m3 pools the others
+// prepare the queries.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const __grid_constant__ WideParams q) {
   asm volatile("griddepcontrol.launch_dependents;");
+  if constexpr (FP8)
+    if (blockIdx.x > 0) {
+      wide_split_queries<D>(q);
+      return;
+    }
   __shared__ int sums[32];
   __shared__ int carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -216,8 +271,9 @@ struct WideWalk {
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__((WideLayout<D, FP8>::THREADS), 1)
-fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const WideParams q) {
+fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q2,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ WideParams q) {
   using L = WideLayout<D, FP8>;
   constexpr int KST = L::KST, VST = L::VST, RST = FP8 ? L::RST : 1;
   const PagedParams& p = q.p;
@@ -252,7 +308,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], FP8 ? 4 : 1);
+      mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[2 * x], 4);
@@ -333,7 +389,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (warp >= 8 && warp < 12) {
     set_regs_dec<L::IO_REGS>();
     if (warp == 11) {
-      // =========================================================== scheduler, and (bf16) producer of the Q tiles
+      // =========================================================== scheduler and producer of the Q tiles
       asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan; everything above overlaps it
       const long long W = (long long)p.plan[p.B * q.n_pairs] * p.Hkv;
       const int sharers = paged_sharers(W, int(gridDim.x));
@@ -358,7 +414,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         walk.fill(q);
       }
       if (lane == 0) {
-        if constexpr (!FP8) prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_q);
+        if constexpr (FP8) prefetch_tmap(&tm_q2);
         int nq[2] = {0, 0};   // Q tiles delivered, per tile
         bool ok = true;
         for (int i = 0; ok; ++i) {
@@ -367,18 +424,21 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           segs[slot] = walk.s;
           mbar_arrive(&seg_full[slot]);
           if (walk.s.cnt == 0) break;
-          if constexpr (!FP8) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (walk.s.blocks[x] == 0) continue;
-              if (nq[x] >= 1 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc)) { ok = false; break; }
-              mbar_arrive_expect_tx(&q_full[x], D * 2 * q.g * q.tq);
+          for (int x = 0; x < 2; ++x) {
+            if (walk.s.blocks[x] == 0) continue;
+            if (nq[x] >= 1 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc)) { ok = false; break; }
+            mbar_arrive_expect_tx(&q_full[x], D * 2 * q.g * q.tq);
+            uint8_t* to = smem + (x ? L::QB_OFF : L::QA_OFF);
+            const int i0 = (2 * walk.s.pair + x) * q.tq, bh = walk.s.b * p.Hkv + walk.s.h;
+            if constexpr (FP8) {
+              tma_load_4d(to, &tm_q, &q_full[x], 0, 0, i0, bh);
+              tma_load_4d(to + L::RAW, &tm_q2, &q_full[x], 0, 0, i0, bh);
+            } else {
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(smem + (x ? L::QB_OFF : L::QA_OFF) + c * L::SUB, &tm_q, &q_full[x], c * 64, 0,
-                            (2 * walk.s.pair + x) * q.tq, walk.s.b * p.Hkv + walk.s.h);
-              ++nq[x];
+              for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * L::SUB, &tm_q, &q_full[x], c * 64, 0, i0, bh);
             }
+            ++nq[x];
           }
           if (ok) walk.next(q);
         }
@@ -544,69 +604,14 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       __syncwarp();
     }
   } else if (FP8 && warp >= 12) {
-    // =========================================================== converters: V to f16, queries to two 8-bit parts
+    // =========================================================== converters: V to f16
     set_regs_dec<L::CVT_REGS>();
     const int ct = tid - 384;
     float* scales = reinterpret_cast<float*>(smem + L::SC_OFF);
-    float* qscale = reinterpret_cast<float*>(smem + L::QS_OFF);
     int gb = 0;        // blocks so far
-    int nq[2] = {0, 0};
     bool ok = true;
     while (ok && next_seg(s)) {
       const int n_max = s.cnt;
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (s.blocks[x] == 0) continue;
-        if (!__all_sync(0xffffffffu, nq[x] < 1 || mbar_wait(&q_empty[x], (nq[x] - 1) & 1, wc))) { ok = false; break; }
-        const int i = (2 * s.pair + x) * q.tq + ct / q.g, jj = ct % q.g;
-        const bool real = ct < q.g * q.tq && i < p.Nq;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + i) * D);
-        float mx = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
-        }
-        // Each row times a power of two that puts its largest element into [2^7, 2^8).  An element's 8 significant bits
-        // are hi = the nearest e4m3 number and at most 8 units of its last bit, which is 3 significant bits: e5m2.
-        // Elements below 2^-9 (2^-17 of the largest) lose bits: at most 2^-14, that is 2^-21 of the largest element.
-        const int ex = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
-        const bool scaled = mx > 0.f && mx < INFINITY;
-        const float up = scaled ? __uint_as_float(uint32_t(127 + 7 - ex) << 23) : 1.f;
-        qscale[((nq[x] & 1) * 2 + x) * 128 + ct] = p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 7 + ex) << 23) : 1.f);
-        uint8_t* dst = smem + (x ? L::QB_OFF : L::QA_OFF);
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint4 w = real ? src[2 * c + y] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float a = __uint_as_float(u[e] << 16) * up, b = __uint_as_float(u[e] & 0xffff0000u) * up;
-              if (!(fabsf(a) < INFINITY)) a = NAN;   // such a row's scores are NaN (inf - inf) in any case
-              if (!(fabsf(b) < INFINITY)) b = NAN;
-              const uint32_t h2 = pack_e4m3x2(a, b), f2 = e4m3x2_to_f16x2(h2);
-              const uint32_t l2 = pack_e5m2x2(a - __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu))),
-                                              b - __half2float(__ushort_as_half((unsigned short)(f2 >> 16))));
-              const int k = 2 * y + (e >> 1);
-              hi[k] = (e & 1) ? hi[k] | (h2 << 16) : h2;
-              lo[k] = (e & 1) ? lo[k] | (l2 << 16) : l2;
-            }
-          }
-          uint8_t* d = dst + PagedLayout<D, true, 1>::at(ct, c);   // the swizzle of a row of D bytes
-          *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(d + L::RAW) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
-        ++nq[x];
-      }
-      if (!ok) break;
       // threads 0-15: K and V scale of 16-key group ct & 7 (past the end 1 and 0: its scores are masked), looked up
       // one block ahead, its page two blocks
       auto group_page = [&](int j) -> int {
@@ -685,6 +690,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // What the block loop needs of the segment; the rest is read again at its end (registers are short here, and
       // with shared memory taking nearly all of L1 a spilled one is a trip to L2).
       int n, key0, lim, lim_lo;
+      float row_scale = 1.f;
       {
         const WideSeg s = read_seg();
         if (s.cnt == 0) break;
@@ -692,10 +698,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         key0 = s.t * 128;
         const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
         const bool stored = ii < q.tq && qi < p.Nq;
+        if (FP8 && stored) row_scale = q.q_scale[((int64_t)(s.b * p.Hkv + s.h) * q.g + jj) * p.Nq + qi];
         lim = stored && qi < s.n ? (p.causal ? max(s.L - s.n + qi + 1, 0) : s.L) : 0;   // keys < lim allowed
         lim_lo = min(p.causal ? s.L - s.n + i0 + 1 : s.L, s.L);                        // the tile's smallest
       }
-      float sl2 = p.scale_log2;
+      const float sl2 = FP8 ? row_scale : p.scale_log2;
       float m_ref = -INFINITY;   // reference max, exp2 domain
       float l = 0.f;
       float vref = 6.0185311e-36f;   // e4m3: the largest value scale so far (2^-117), O is in units of it
@@ -750,7 +757,6 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if constexpr (FP8) {
           // The scores are read twice, 64 at a time (registers and instruction cache are short here).  sc: K's scales
           // of the block's 8 groups of 16 keys, then V's.
-          if (j == 0) sl2 = *reinterpret_cast<const volatile float*>(smem + L::QS_OFF + (((ni & 1) * 2 + x) * 128 + r) * 4);
           const int b = gb + j;
           if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[b % L::SST], (b / L::SST) & 1, wc))) { ok = false; break; }
           const uint32_t sc = smem_u32(smem) + L::SC_OFF + (b % L::SST) * 64;
