@@ -34,7 +34,7 @@ struct WideParams {
 };
 
 // A segment: consecutive blocks of one pair, as much of it as falls into the CTA's share.
-struct WideSeg {
+struct alignas(16) WideSeg {
   int b, h, pair, t, T;   // t: its first block, T: blocks of the pair
   int L, n, cnt;          // keys and new tokens of the sequence, blocks of the segment (0: the share is done)
   int blocks[2];          // blocks of either tile in it
@@ -63,7 +63,7 @@ struct WideLayout {
   static constexpr int SEGS = 4;                   // segments scheduled ahead
   static constexpr int NBARS = 4 + 2 * KST + 2 * VST + 2 * RST + 2 + 4 + 2 + 2 + 2 + 2 * SEGS + (FP8 ? SST : 0);
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int SEG_OFF = MISC_OFF + 16;
+  static constexpr int SEG_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
   static constexpr int BYTES = SEG_OFF + SEGS * int(sizeof(WideSeg));
   __device__ static constexpr int s_col(int x) { return 128 * x; }
   __device__ static constexpr int o_col(int x) { return 256 + D * x; }
@@ -355,10 +355,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   int seg_at = 0;
   auto read_seg = [&]() {
     WideSeg s;
-    const volatile int* from = reinterpret_cast<const volatile int*>(&segs[seg_at % L::SEGS]);
-    int* to = reinterpret_cast<int*>(&s);
-#pragma unroll
-    for (int i = 0; i < int(sizeof(WideSeg) / 4); ++i) to[i] = from[i];
+    const uint32_t at = smem_u32(&segs[seg_at % L::SEGS]);
+    asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(s.b), "=r"(s.h), "=r"(s.pair), "=r"(s.t) : "r"(at) : "memory");
+    asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(s.T), "=r"(s.L), "=r"(s.n), "=r"(s.cnt) : "r"(at + 16) : "memory");
+    asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(s.blocks[0]), "=r"(s.blocks[1]), "=r"(s.first), "=r"(s.pad) : "r"(at + 32) : "memory");
     return s;
   };
   auto wait_seg = [&]() {
@@ -515,13 +516,13 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const uint32_t s0 = smem_u32(smem) >> 4;
       constexpr uint32_t kHi = sdesc_sw128_hi(1024), kKM = sdesc_lbo(16), kMN = sdesc_lbo(L::SUB);
       int gk = 0;                // blocks consumed (K and V alike)
-      int nb[2] = {0, 0};        // blocks of each tile so far: phase of p_full
-      int ni[2] = {0, 0};        // segments with work for each tile so far: phase of q_full, o_free
+      int nb0 = 0, nb1 = 0;      // blocks of either tile so far: phase of p_full
+      int ni0 = 0, ni1 = 0;      // segments with work for either tile so far: phase of q_full, o_free
       bool ok = true;
       while (ok && next_seg(s)) {
-        const int n_x[2] = {s.blocks[0], s.blocks[1]}, n_max = s.cnt;
+        const int n_max = s.cnt;
         auto issue_s = [&](int x, int kst) {   // S_x = Q_x K^T
-          const uint32_t q_lo = s0 + uint32_t((x ? L::QB_OFF : L::QA_OFF) >> 4) + kKM;
+          const uint32_t q_lo = s0 + uint32_t((L::QA_OFF + x * L::TILE) >> 4) + kKM;
           const uint32_t k_lo = s0 + uint32_t((L::K_OFF + kst * L::KTILE) >> 4) + kKM;
           if constexpr (FP8) {
             // rows of D bytes: the 128-byte swizzle at D = 128, the 64-byte swizzle (layout 4, 8 rows 512 bytes apart) at 64
@@ -539,65 +540,114 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               mma_ss_elect(tmem + L::s_col(x), sdesc_join(q_lo + off, kHi), sdesc_join(k_lo + off, kHi), kIdS, kk > 0 ? 1u : 0u);
             }
           }
-        };
-        auto issue_pv_half = [&](int x, int vst, int h, uint32_t acc0) {   // O_x += P_x[keys of half h] V[same keys]
-          const uint32_t v_lo = s0 + uint32_t((L::V_OFF + vst * L::TILE) >> 4) + kMN;
-#pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_ts_elect(tmem + L::o_col(x), tmem + L::s_col(x) + kk * 8, sdesc_join(v_lo + kk * (2048 >> 4), kHi), kIdPV,
-                         kk > 0 ? 1u : acc0);
-        };
-        if (!wait(&k_full[gk % KST], (gk / KST) & 1)) { ok = false; break; }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (n_x[x] == 0) continue;
-          if (!wait(&q_full[x], ni[x] & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_s(x, gk % KST);
           mma_commit_elect(&s_full[x]);
-          if (n_x[x] == 1) mma_commit_elect(&q_empty[x]);   // the next segment's Q_x may come now
-        }
-        if (!ok) break;
-        mma_commit_elect(&k_empty[gk % KST]);
-        for (int j = 0; ok && j < n_max; ++j) {
-          const int vst = (gk + j) % VST, kst1 = (gk + j + 1) % KST;
-          if (!wait(&v_full[vst], ((gk + j) / VST) & 1)) { ok = false; break; }
-          bool have_k = false;   // K_{j+1} resident
+        };
+        if constexpr (FP8) {
+          // Rolled over the tiles and the halves of P, since code that runs once a segment comes from beyond the instruction
+          // cache, at a microsecond a stretch (2 x 16 x 4096 prefill 261 -> 224 us).  bf16, with less code in its other warps,
+          // loses more by the loops (chunk of 512: 190 -> 214 us).
+          // step -1: the first S of either tile; step j: PV(j), then S(j + 1)
+          for (int j = -1; ok && j < n_max; ++j) {
+            const int vst = (gk + j) % VST, kst1 = (gk + j + 1) % KST;
+            if (j >= 0 && !wait(&v_full[vst], ((gk + j) / VST) & 1)) { ok = false; break; }
+            bool have_k = false;   // K_{j+1} resident
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              const int n_x = x ? s.blocks[1] : s.blocks[0], n_i = x ? ni1 : ni0, n_b = x ? nb1 : nb0;
+              if (j >= n_x || n_x == 0) continue;
+              if (j >= 0) {
+                // the first PV of a segment overwrites O: the previous segment's epilogue must have read it
+                if (j == 0 && n_i >= 1 && !wait(&o_free[x], (n_i - 1) & 1)) { ok = false; break; }
+                const uint32_t v_lo = s0 + uint32_t((L::V_OFF + vst * L::TILE) >> 4) + kMN;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {   // O_x += P_x[keys of half h] V[same keys]
+                  if (!wait(&p_full[2 * x + h], (n_b + j) & 1)) { ok = false; break; }
+                  tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j >= n_x[x]) continue;
-            // the first PV of a segment overwrites O: the previous segment's epilogue must have read it
-            if (j == 0 && ni[x] >= 1 && !wait(&o_free[x], (ni[x] - 1) & 1)) { ok = false; break; }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!wait(&p_full[2 * x + h], (nb[x] + j) & 1)) { ok = false; break; }
-              tc_fence_after();
-              issue_pv_half(x, vst, h, j > 0 ? 1u : 0u);
+                  for (int k = 0; k < 4; ++k)
+                    mma_ts_elect(tmem + L::o_col(x), tmem + L::s_col(x) + 32 * h + k * 8,
+                                 sdesc_join(v_lo + (4 * h + k) * (2048 >> 4), kHi), kIdPV, (j > 0 || h + k > 0) ? 1u : 0u);
+                }
+                if (!ok) break;
+              } else if (!wait(&q_full[x], n_i & 1)) {
+                ok = false;
+                break;
+              }
+              if (j + 1 < n_x) {
+                if (!have_k) {
+                  if (!wait(&k_full[kst1], ((gk + j + 1) / KST) & 1)) { ok = false; break; }
+                  have_k = true;
+                }
+                tc_fence_after();
+                issue_s(x, kst1);
+                if (j + 2 == n_x) mma_commit_elect(&q_empty[x]);   // the next segment's Q_x may come now
+              } else {
+                mma_commit_elect(&o_fin[x]);
+              }
             }
             if (!ok) break;
-            if (j + 1 < n_x[x]) {
-              if (!have_k) {
-                if (!wait(&k_full[kst1], ((gk + j + 1) / KST) & 1)) { ok = false; break; }
-                tc_fence_after();
-                have_k = true;
-              }
-              issue_s(x, kst1);
-              mma_commit_elect(&s_full[x]);
-              if (j + 2 == n_x[x]) mma_commit_elect(&q_empty[x]);
-            } else {
-              mma_commit_elect(&o_fin[x]);
-            }
+            if (j >= 0) mma_commit_elect(&v_empty[vst]);           // V_j: both tiles' PV issued
+            if (j + 1 < n_max) mma_commit_elect(&k_empty[kst1]);   // K_{j+1}: both tiles' S issued
+          }
+        } else {
+          const int n_x[2] = {s.blocks[0], s.blocks[1]}, n_i[2] = {ni0, ni1}, n_b[2] = {nb0, nb1};
+          auto issue_pv_half = [&](int x, int vst, int h, uint32_t acc0) {   // O_x += P_x[keys of half h] V[same keys]
+            const uint32_t v_lo = s0 + uint32_t((L::V_OFF + vst * L::TILE) >> 4) + kMN;
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_ts_elect(tmem + L::o_col(x), tmem + L::s_col(x) + kk * 8, sdesc_join(v_lo + kk * (2048 >> 4), kHi), kIdPV,
+                           kk > 0 ? 1u : acc0);
+          };
+          if (!wait(&k_full[gk % KST], (gk / KST) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (n_x[x] == 0) continue;
+            if (!wait(&q_full[x], n_i[x] & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_s(x, gk % KST);
+            if (n_x[x] == 1) mma_commit_elect(&q_empty[x]);   // the next segment's Q_x may come now
           }
           if (!ok) break;
-          mma_commit_elect(&v_empty[vst]);                       // V_j: both tiles' PV issued
-          if (j + 1 < n_max) mma_commit_elect(&k_empty[kst1]);   // K_{j+1}: both tiles' S issued
+          mma_commit_elect(&k_empty[gk % KST]);
+          for (int j = 0; ok && j < n_max; ++j) {
+            const int vst = (gk + j) % VST, kst1 = (gk + j + 1) % KST;
+            if (!wait(&v_full[vst], ((gk + j) / VST) & 1)) { ok = false; break; }
+            bool have_k = false;   // K_{j+1} resident
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (j >= n_x[x]) continue;
+              // the first PV of a segment overwrites O: the previous segment's epilogue must have read it
+              if (j == 0 && n_i[x] >= 1 && !wait(&o_free[x], (n_i[x] - 1) & 1)) { ok = false; break; }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!wait(&p_full[2 * x + h], (n_b[x] + j) & 1)) { ok = false; break; }
+                tc_fence_after();
+                issue_pv_half(x, vst, h, j > 0 ? 1u : 0u);
+              }
+              if (!ok) break;
+              if (j + 1 < n_x[x]) {
+                if (!have_k) {
+                  if (!wait(&k_full[kst1], ((gk + j + 1) / KST) & 1)) { ok = false; break; }
+                  tc_fence_after();
+                  have_k = true;
+                }
+                issue_s(x, kst1);
+                if (j + 2 == n_x[x]) mma_commit_elect(&q_empty[x]);
+              } else {
+                mma_commit_elect(&o_fin[x]);
+              }
+            }
+            if (!ok) break;
+            mma_commit_elect(&v_empty[vst]);                       // V_j: both tiles' PV issued
+            if (j + 1 < n_max) mma_commit_elect(&k_empty[kst1]);   // K_{j+1}: both tiles' S issued
+          }
+          if (!ok) break;
         }
         gk += n_max;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          nb[x] += n_x[x];
-          ni[x] += (n_x[x] > 0);
-        }
+        nb0 += s.blocks[0];
+        nb1 += s.blocks[1];
+        ni0 += s.blocks[0] > 0;
+        ni1 += s.blocks[1] > 0;
       }
       mma_commit_elect(fin);   // completes when every MMA issued above has finished
       if (lane == 0) mbar_drain(fin, 0, q.wait_ns);
@@ -633,11 +683,6 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (gb / RST) & 1, wc))) { ok = false; break; }
         constexpr int CPR = D / 16;   // raw 16-byte chunks per key, and chunks per thread
         const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
-        uint4 w[CPR];
-#pragma unroll
-        for (int i = 0; i < CPR; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (i * 128 + ct) * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[st]);
         // (a free stage also means that block gb - VST is done with: its scales, SST blocks back, too)
         if (!__all_sync(0xffffffffu, gb < VST || mbar_wait(&v_empty[dst_st], ((gb / VST) - 1) & 1, wc))) { ok = false; break; }
         if (warp == 12) {
@@ -646,10 +691,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (lane == 0) mbar_arrive(&sc_full[gb % L::SST]);
         }
         uint8_t* dst = smem + L::V_OFF + dst_st * L::TILE;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < CPR; ++i) {
           const int id = i * 128 + ct, row = id / CPR, c = id % CPR;
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + id * 16);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
           uint32_t o[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -671,7 +717,10 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[dst_st]);
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[st]);
+          mbar_arrive(&v_full[dst_st]);
+        }
       }
     }
   } else {
@@ -694,7 +743,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       {
         const WideSeg s = read_seg();
         if (s.cnt == 0) break;
-        n = s.blocks[x];
+        n = x ? s.blocks[1] : s.blocks[0];
         key0 = s.t * 128;
         const int i0 = (2 * s.pair + x) * q.tq, qi = i0 + ii;
         const bool stored = ii < q.tq && qi < p.Nq;
@@ -872,7 +921,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       float zero = 0.f;   // stays 0 unless O has a value that is not finite
       const float f = l != 0.f ? (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? 1.f / l : 1.f) : 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t orr[32];
         if (n > 0) {
