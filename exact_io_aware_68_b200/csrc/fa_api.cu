@@ -547,8 +547,9 @@ fa_status launch_paged(fa::WideParams q, int sms, cudaStream_t s) {
   q.p.n_warps = ctas * Lt::WARPS;
   fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, NG>, Lt::bytes(fa::kPagedMaxB));
   if (st != FA_OK) return st;
-  fa::fa_paged_split_kernel<D, FP8, NG><<<ctas, 32 * Lt::WARPS, Lt::bytes(q.p.B), s>>>(q.p);
-  if ((st = launch_status("fa_fwd_paged split kernel launch")) != FA_OK) return st;
+  st = launch_dependent<fa::PagedParams>(fa::fa_paged_split_kernel<D, FP8, NG>, unsigned(ctas), 32 * Lt::WARPS,
+                                         unsigned(Lt::bytes(q.p.B)), s, "fa_fwd_paged split kernel launch", q.p);
+  if (st != FA_OK) return st;
   return launch_paged_combine<D>(q.p, 8 * NG, sms, s);
 }
 
@@ -606,8 +607,9 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   if ((st = check_launch_regs(kernel, L::LAUNCH_REGS, "fa_fwd_paged wide kernel")) != FA_OK) return st;
   // one CTA plans; e4m3: the others, at most two per SM, prepare the queries, D / 8 threads a row
   const int64_t split = FP8 ? std::min<int64_t>((rows + 8191 / D) / (8192 / D), 2 * sms) : 0;
-  fa::fa_paged_plan_kernel<D, FP8><<<unsigned(1 + split), 1024, 0, s>>>(q);
-  if ((st = launch_status("fa_fwd_paged plan kernel launch")) != FA_OK) return st;
+  st = launch_dependent<fa::WideParams>(fa::fa_paged_plan_kernel<D, FP8>, unsigned(1 + split), 1024, 0, s,
+                                        "fa_fwd_paged plan kernel launch", q);
+  if (st != FA_OK) return st;
   st = launch_dependent<CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, fa::WideParams>(
       kernel, unsigned(paged_ctas(sms)), unsigned(L::THREADS), unsigned(L::BYTES), s, "fa_fwd_paged wide kernel launch", mq, mq2, mk, mv, q);
   if (st != FA_OK) return st;
@@ -780,8 +782,7 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   };
   if (!fp8) {
     rows(128);
-    fa::fa_kv_append_kernel<<<p.row_blocks, 128, 0, s>>>(p);
-    return launch_status("fa_kv_append kernel launch");
+    return launch_dependent<fa::AppendParams>(fa::fa_kv_append_kernel, unsigned(p.row_blocks), 128, 0, s, "fa_kv_append kernel launch", p);
   }
   p.touched = (Nq + page_size - 2) / page_size + 1;
   const int most = Nq < page_size ? Nq : page_size;   // new rows of one page
@@ -792,14 +793,13 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   const int64_t blocks = p.row_blocks + int64_t(B) * p.touched * Hkv * 2;
   if (blocks >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "too many pages to append to (%lld)", (long long)blocks);
   const unsigned grid = unsigned(blocks);
-  switch (threads) {
-    case 32: fa::fa_kv_append_e4m3_kernel<32><<<grid, 32, 0, s>>>(p); break;
-    case 64: fa::fa_kv_append_e4m3_kernel<64><<<grid, 64, 0, s>>>(p); break;
-    case 128: fa::fa_kv_append_e4m3_kernel<128><<<grid, 128, 0, s>>>(p); break;
-    case 256: fa::fa_kv_append_e4m3_kernel<256><<<grid, 256, 0, s>>>(p); break;
-    default: fa::fa_kv_append_e4m3_kernel<512><<<grid, 512, 0, s>>>(p); break;
-  }
-  return launch_status("fa_kv_append_e4m3 kernel launch");
+  const char* what = "fa_kv_append_e4m3 kernel launch";
+  auto kernel = threads == 32    ? fa::fa_kv_append_e4m3_kernel<32>
+                : threads == 64  ? fa::fa_kv_append_e4m3_kernel<64>
+                : threads == 128 ? fa::fa_kv_append_e4m3_kernel<128>
+                : threads == 256 ? fa::fa_kv_append_e4m3_kernel<256>
+                                 : fa::fa_kv_append_e4m3_kernel<512>;
+  return launch_dependent<fa::AppendParams>(kernel, grid, unsigned(threads), 0, s, what, p);
 }
 
 unsigned grid_for(uint64_t work, unsigned per_block) {

@@ -169,7 +169,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
   }
 }
 
-__global__ void __launch_bounds__(128) fa_kv_append_kernel(const AppendParams p) { append_rows<true>(p, int(blockIdx.x)); }
+__global__ void __launch_bounds__(128) fa_kv_append_kernel(const __grid_constant__ AppendParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // (a programmatic dependent launch)
+  append_rows<true>(p, int(blockIdx.x));
+}
 
 // ----------------------------------------------------------------------------- e4m3 pages
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {   // nearest, saturating; NaN stays NaN
@@ -194,7 +197,8 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 // (at most 4 per thread) between the search for the scale and the rounding, as the bf16 they came in: rotating
 // them twice costs less than the registers of the results.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) fa_kv_append_e4m3_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) fa_kv_append_e4m3_kernel(const __grid_constant__ AppendParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (int(blockIdx.x) < p.row_blocks) {
     append_rows<false>(p, int(blockIdx.x));
     return;

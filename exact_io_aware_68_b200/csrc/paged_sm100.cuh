@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   extern __shared__ __align__(1024) uint8_t smem[];
   int* off = reinterpret_cast<int*>(smem + Lt::RING);   // [B + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a programmatic dependent launch: the kernel before it on the stream has to be complete from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- prefix of the sequences' key tiles: every thread sums a run of sequences, then the runs are scanned

@@ -172,6 +172,7 @@ __device__ __forceinline__ void wide_split_queries(const WideParams& q) {
 // prepare the queries.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const __grid_constant__ WideParams q) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   if constexpr (FP8)
     if (blockIdx.x > 0) {
