@@ -198,6 +198,16 @@ fa_status set_smem(K kernel, int bytes) {
   return FA_OK;
 }
 
+// The same, asked of the runtime once per device and kernel (`done`: a bit per device).
+template <typename K>
+fa_status set_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && (done.load() >> dev & 1)) return FA_OK;
+  const fa_status st = set_smem(kernel, bytes);
+  if (st == FA_OK && dev >= 0 && dev < 64) done.fetch_or(uint64_t(1) << dev);
+  return st;
+}
+
 // The warp-specialised kernels re-split their registers per warpgroup with setmaxnreg; the split
 // adds up to `regs` registers per thread at launch.  A build whose kernel was given fewer
 // registers would leave a setmaxnreg.inc waiting forever, so it is refused before the launch.
@@ -545,7 +555,8 @@ fa_status launch_paged(fa::WideParams q, int sms, cudaStream_t s) {
   static_assert(Lt::WARPS <= kPagedMostWarps && Lt::bytes(fa::kPagedMaxB) <= 232448, "workspace, shared memory");
   const int ctas = paged_ctas(sms);
   q.p.n_warps = ctas * Lt::WARPS;
-  fa_status st = set_smem(fa::fa_paged_split_kernel<D, FP8, NG>, Lt::bytes(fa::kPagedMaxB));
+  static std::atomic<uint64_t> smem_set{0};
+  fa_status st = set_smem_once(fa::fa_paged_split_kernel<D, FP8, NG>, Lt::bytes(fa::kPagedMaxB), smem_set);
   if (st != FA_OK) return st;
   st = launch_dependent<fa::PagedParams>(fa::fa_paged_split_kernel<D, FP8, NG>, unsigned(ctas), 32 * Lt::WARPS,
                                          unsigned(Lt::bytes(q.p.B)), s, "fa_fwd_paged split kernel launch", q.p);

@@ -155,7 +155,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, key_lens, new_lens=None, rope=
         q_ptr = out_ptr = None
     else:
         if q_out is None:
-            q_out = torch.empty((B, Hq, Nq, d), dtype=bf16, device=k_cache.device)
+            q_out = torch.empty_strided((B, Hq, Nq, d), (Hq * Nq * d, Nq * d, d, 1), dtype=bf16, device=k_cache.device)
         elif not _fits(q_out, bf16, q.shape, dev):
             raise ValueError(f"q_out must be contiguous bfloat16 {tuple(q.shape)} on {k_cache.device}")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -195,11 +195,11 @@ def attention_paged(q, k_cache, v_cache, page_table, key_lens, scale=None, causa
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError(f"workspace must be contiguous uint8 on {device}")
     if o is None:
-        o = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        o = torch.empty_like(q)   # q is contiguous
     elif not _fits(o, torch.bfloat16, shape, dev):
         raise ValueError(f"o must be contiguous bfloat16 {tuple(shape)} on {device}")
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+        lse = torch.empty_strided((B, Hq, Nq), (Hq * Nq, Nq, 1), dtype=torch.float32, device=device)
     elif not _fits(lse, torch.float32, shape[:3], dev):
         raise ValueError(f"lse must be contiguous float32 {tuple(shape[:3])} on {device}")
     name, scales = ("fa_fwd_paged", ()) if k_scale is None else ("fa_fwd_paged_e4m3", (k_scale.data_ptr(), v_scale.data_ptr()))
