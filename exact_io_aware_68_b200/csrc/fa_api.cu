@@ -784,15 +784,18 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   const int64_t tokens = int64_t(B) * Nq;
   // the row role's blocks hold `threads` threads of d / 16 per token; a thread takes up to 8 heads of its token
   // as long as that leaves about 2048 threads per SM
-  auto rows = [&](int threads) {
+  auto rows = [&](int threads) -> int64_t {
     const int per = threads / (d / 16);
-    p.row_blocks_x = int((tokens + per - 1) / per);
+    const int64_t x = (tokens + per - 1) / per;
     p.heads_per_thread = 1;
     while (p.heads_per_thread < 8 && tokens * (d / 16) * heads / (2 * p.heads_per_thread) >= 148 * 2048) p.heads_per_thread *= 2;
-    p.row_blocks = heads == 0 ? 0 : p.row_blocks_x * ((heads + p.heads_per_thread - 1) / p.heads_per_thread);
+    const int64_t blocks = heads == 0 ? 0 : x * ((heads + p.heads_per_thread - 1) / p.heads_per_thread);
+    p.row_blocks_x = int(x);
+    p.row_blocks = int(blocks);
+    return blocks;
   };
   if (!fp8) {
-    rows(128);
+    if (rows(128) >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "B * Nq = %lld tokens are too many", (long long)tokens);
     return launch_dependent<fa::AppendParams>(fa::fa_kv_append_kernel, unsigned(p.row_blocks), 128, 0, s, "fa_kv_append kernel launch", p);
   }
   p.touched = (Nq + page_size - 2) / page_size + 1;
@@ -800,8 +803,7 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   const int lpr = d / 16;
   int threads = 32;
   while (threads / lpr * 4 < most) threads *= 2;
-  rows(threads);
-  const int64_t blocks = p.row_blocks + int64_t(B) * p.touched * Hkv * 2;
+  const int64_t blocks = rows(threads) + int64_t(B) * p.touched * Hkv * 2;
   if (blocks >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "too many pages to append to (%lld)", (long long)blocks);
   const unsigned grid = unsigned(blocks);
   const char* what = "fa_kv_append_e4m3 kernel launch";

@@ -137,6 +137,9 @@ ATTENTION = [
     (2, 1, 2, 70, 128, 16, [70, 513], [70, 33], True),
     (1, 1, 8, 16, 64, 64, [500], None, False),
     (33, 1, 2, 1, 128, 16, [16 * (i % 5) + i for i in range(33)], None, True),
+    (700, 1, 1, 1, 64, 16, [(7 * i) % 40 for i in range(700)], None, True),
+    (2, 2, 8, 4, 64, 32, [400, 35], [4, 2], True),
+    (2, 1, 6, 4, 128, 16, [300, 4], None, True),
     (2, 1, 1, 2, 64, 16, [1, 3], [2, 2], True),     # a query before position 0 sees nothing
     (2, 1, 3, 300, 128, 64, [300, 1000], [300, 211], True),
     (1, 1, 8, 40, 64, 16, [5000], None, True),
@@ -234,12 +237,13 @@ def test_attention_equals_contiguous_decode():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
-def test_attention_repeats_bit_for_bit(fp8):
+@pytest.mark.parametrize("Nq", [1, 2, 4, 30])
+def test_attention_repeats_bit_for_bit(Nq, fp8):
     """No atomics: the same inputs give the same bits, also out of a workspace full of NaN."""
     lens = [5000, 300, 77]
     cache = Cache(3, 2, 64, 16, lens, fp8, seed=11)
-    q = bf16(torch.randn((3, 12, 2, 64), generator=cache.g)).cuda()
-    ws = fa.paged_workspace(3, 12, 2, 2, 64, "cuda")
+    q = bf16(torch.randn((3, 12, Nq, 64), generator=cache.g)).cuda()
+    ws = fa.paged_workspace(3, 12, 2, Nq, 64, "cuda")
     got = []
     for fill in (0, 0xFF):
         ws.fill_(fill)
@@ -473,22 +477,130 @@ def test_serving_loop_in_a_captured_graph(fp8):
 
 
 @pytest.mark.gpu
-def test_two_streams_with_workspaces_of_their_own():
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_two_streams_with_workspaces_of_their_own(Nq, fp8):
     lens = [3000, 50]
-    cache = Cache(2, 2, 128, 32, lens, False, seed=13)
-    q = bf16(torch.randn((2, 8, 1, 128), generator=cache.g)).cuda()
-    want = fa.attention_paged(q, *cache.args(), i32(lens))
+    cache = Cache(2, 2, 128, 32, lens, fp8, seed=13)
+    q = bf16(torch.randn((2, 8, Nq, 128), generator=cache.g)).cuda()
+    want = fa.attention_paged(q, *cache.args(), i32(lens), causal=True, **cache.scales())
     kl = i32(lens)
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
     got = []
     for s in streams * 4:
         with torch.cuda.stream(s):
-            got.append(fa.attention_paged(q, *cache.args(), kl))
+            got.append(fa.attention_paged(q, *cache.args(), kl, causal=True, **cache.scales()))
     torch.cuda.synchronize()
     fa.check()
     for o, lse in got:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_chunks_of_a_prompt_in_a_captured_graph(fp8):
+    """A prompt appended and attended to in padded chunks by one replayed graph, against the whole at once."""
+    B, Hq, Hkv, d, page, chunk, steps = 2, 8, 2, 128, 64, 48, 3
+    total = [chunk * steps, 100]   # the second prompt ends within the last chunk
+    g = torch.Generator().manual_seed(31)
+    x = bf16(torch.randn((B, chunk * steps, Hq + 2 * Hkv, d), generator=g)).cuda()
+    rope = tuple(t.cuda() for t in fa.rope_tables(chunk * steps, d, device="cpu"))
+
+    def heads(y):
+        y = y.transpose(1, 2)
+        return y[:, :Hq], y[:, Hq: Hq + Hkv], y[:, Hq + Hkv:]
+
+    whole, parts = (Cache(B, Hkv, d, page, [0, 0], fp8, seed=17, room=chunk * steps) for _ in range(2))
+    q, k, v = heads(x)
+    kl = i32(total)
+    qr = fa.kv_append(k, v, *whole.args(), kl, new_lens=kl, rope=rope, q=q, **whole.scales())
+    want, want_lse = fa.attention_paged(qr, *whole.args(), kl, causal=True, new_lens=kl, **whole.scales())
+    kl, nl, y = i32([0, 0]), i32([0, 0]), torch.zeros_like(x[:, :chunk])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        q, k, v = heads(y)
+        qr = fa.kv_append(k, v, *parts.args(), kl, new_lens=nl, rope=rope, q=q, **parts.scales())
+        o, lse = fa.attention_paged(qr, *parts.args(), kl, causal=True, new_lens=nl, **parts.scales())
+    for i in range(steps):
+        n = [max(0, min(chunk, t - i * chunk)) for t in total]
+        nl.copy_(i32(n))
+        kl.add_(nl)
+        y.copy_(x[:, i * chunk: (i + 1) * chunk])
+        graph.replay()
+        torch.cuda.synchronize()
+        fa.check()
+        for b in range(B):
+            a, w = o[b, :, : n[b]].float(), want[b, :, i * chunk: i * chunk + n[b]].float()
+            assert not o[b, :, n[b]:].any() and torch.isneginf(lse[b, :, n[b]:]).all()
+            if n[b] == 0:
+                continue
+            # the same function of the same values; e4m3 pages that grew by chunks hold codes that were re-rounded
+            # (half a step of 2^-4 of a value, twice), bf16 ones the very same keys: two roundings of O, P in bf16
+            tol = 0.25 if fp8 else 2.0 ** -6
+            assert (a - w).abs().max() <= tol * w.abs().max().clamp(min=1)
+            assert (a - w).norm() <= (0.06 if fp8 else 2.0 ** -7) * w.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_pools_beyond_32_bit_offsets(fp8, Nq):
+    """Pages that lie more than 2^32 bytes into their pool."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    B, Hkv, group, d, page, lens = 2, 8, 4, 128, 64, [150, 64]
+    small = Cache(B, Hkv, d, page, lens, fp8, seed=41)
+    per = Hkv * page * d * (1 if fp8 else 2)
+    far = (1 << 32) // per + 5   # page numbers from here on
+    n = far + small.n_pages
+    pools, scales = {}, {}
+    for c in "kv":
+        pools[c] = torch.zeros((n, Hkv, page, d), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+        pools[c][far:] = small.dev[c].view(pools[c].dtype)
+        pools[c] = pools[c].view(small.pool[c].dtype)
+        if fp8:
+            scales[c + "_scale"] = torch.ones((n, Hkv), device="cuda")
+            scales[c + "_scale"][far:] = small.sdev[c]
+    table = (small.table_dev + far).clamp(max=1 << 30)
+    q = bf16(torch.randn((B, Hkv * group, Nq, d), generator=small.g))
+    o, lse = fa.attention_paged(q.cuda(), pools["k"], pools["v"], table, i32(lens), causal=True, **scales)
+    fa.check()
+    check_attention(small, q, lens, [Nq] * B, True, o, lse, group * Nq)
+    # and an append: the last row of sequence 0 again
+    x = bf16(torch.randn((B, Hkv, 1, d), generator=small.g)).cuda()
+    fa.kv_append(x, x, pools["k"], pools["v"], table, i32(lens), new_lens=i32([1, 0]), **scales)
+    fa.check()
+    at = (int(table[0, 149 // page]), slice(None), 149 % page)
+    for c in "kv":
+        if fp8:
+            got = pools[c].view(torch.uint8)[at].view(torch.float8_e4m3fn).float() * scales[c + "_scale"][at[0]][:, None]
+            assert ((got - x[0, :, 0].float()).abs() <= 2.0 ** -4 * x[0, :, 0].float().abs() + scales[c + "_scale"][at[0]][:, None] * 2.0 ** -10).all()
+        else:
+            assert torch.equal(pools[c][at], x[0, :, 0])
+
+
+@pytest.mark.gpu
+def test_append_keeps_a_callers_scale():
+    """A scale that is no power of two stays while it suffices, and its codes with it."""
+    cache = Cache(1, 2, 64, 16, [3], True, seed=51, room=8)
+    i = int(cache.table[0, 0])
+    for c in "kv":
+        cache.scale[c][i] = cache.scale[c][i] * 2.75
+        cache.sdev[c] = cache.scale[c].cuda()
+        cache.val[c][i] = oracle.E4M3[cache.pool[c].view(torch.uint8).numpy()[i]] * cache.scale[c][i].double().numpy()[:, None, None]
+    k, v = (bf16(0.5 * torch.randn((1, 2, 2, 64), generator=cache.g)) for _ in "kv")
+    check_append(cache, None, k, v, [5], [2], None, False, run_append(cache, None, k, v, [5], [2], None, False))
+    k, v = (bf16(100 * torch.randn((1, 2, 2, 64), generator=cache.g)) for _ in "kv")
+    for c in "kv":
+        cache.pool[c], cache.scale[c] = cache.dev[c].cpu().clone(), cache.sdev[c].cpu().clone()
+        cache.val[c] = oracle.E4M3[cache.pool[c].view(torch.uint8).numpy()] * cache.scale[c].double().numpy()[:, :, None, None]
+    out = run_append(cache, None, k, v, [7], [2], None, False)
+    # codes * (s / s'): the product with a scale that is no power of two is rounded to fp32 before it is encoded
+    for c in "kv":
+        cache.val[c] = np.float64(np.float32(cache.val[c]))
+    check_append(cache, None, k, v, [7], [2], None, False, out)
 
 
 # ----------------------------------------------------------------------------- refusals
@@ -519,7 +631,7 @@ def c_append(lib, fp8=False, **over):
 INV, UNS = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED
 SHARED = [(dict(B=0), INV), (dict(Nq=0), INV), (dict(Hkv=0), INV), (dict(n_pages=0), INV), (dict(max_pages=0), INV), (dict(Hq=3, Hkv=2), INV),
           (dict(d=96), UNS), (dict(d=256), UNS), (dict(page=8), UNS), (dict(page=48), UNS), (dict(page=512), UNS), (dict(B=5000), UNS),
-          (dict(B=4096, Hq=32), UNS), (dict(B=64, max_pages=1 << 21), UNS), (dict(kp=1023), INV), (dict(vp=1025), INV), (dict(table=0), INV),
+          (dict(B=4096, Hq=32), UNS), (dict(B=64, max_pages=1 << 21), UNS), (dict(kp=1023), INV), (dict(vp=1025), INV), (dict(kp=1 << 31), UNS), (dict(table=0), INV),
           (dict(lens=0), INV)]
 
 
