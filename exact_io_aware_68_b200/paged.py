@@ -29,27 +29,23 @@ def _need(ok, text):
 
 def _cache_fits(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d, dev):
     """Whether the cache's tensors fit one another: the quick form of ``_refuse_cache``, which says what does not."""
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[3] != d or v_cache.shape != shape or not k_cache.is_cuda:
+    shape, dt = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or dev < 0:
         return False
-    inner = (shape[2] * d, d, 1)
-    dt = k_cache.dtype
+    n_pages, heads, page, dd = shape
+    inner = (page * d, d, 1)
+    if dd != d or v_cache.shape != shape or v_cache.dtype is not dt or k_cache.stride()[1:] != inner or v_cache.stride()[1:] != inner \
+            or v_cache.get_device() != dev:
+        return False
     if dt is torch.float8_e4m3fn:
-        if k_scale is None or v_scale is None:
-            return False
-        pages = shape[:2]
-        if not (k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32 and k_scale.shape == pages and v_scale.shape == pages
-                and k_scale.is_contiguous() and v_scale.is_contiguous() and k_scale.get_device() == dev == v_scale.get_device()):
+        pages = (n_pages, heads)
+        if k_scale is None or v_scale is None or not (_fits(k_scale, torch.float32, pages, dev) and _fits(v_scale, torch.float32, pages, dev)):
             return False
     elif dt is not torch.bfloat16 or k_scale is not None or v_scale is not None:
         return False
-    if new_lens is not None and not (new_lens.dtype is torch.int32 and new_lens.shape == (B,) and new_lens.is_contiguous()
-                                     and new_lens.get_device() == dev):
-        return False
-    return (v_cache.dtype is dt and k_cache.stride()[1:] == inner and v_cache.stride()[1:] == inner and v_cache.get_device() == dev
-            and key_lens.dtype is torch.int32 and key_lens.shape == (B,) and key_lens.is_contiguous() and key_lens.get_device() == dev
-            and page_table.dtype is torch.int32 and page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_contiguous()
-            and page_table.get_device() == dev)
+    i32, rows = torch.int32, (B,)
+    return (_fits(key_lens, i32, rows, dev) and (new_lens is None or _fits(new_lens, i32, rows, dev)) and page_table.dtype is i32
+            and page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_contiguous() and page_table.get_device() == dev)
 
 
 def _refuse_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_lens, B, d):
@@ -82,13 +78,20 @@ def _fits(t, dtype, shape, dev):
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
 
 
+@functools.cache
+def _entry(name):
+    return getattr(_lib.load(), name)
+
+
 def _call(dev, name, *args):
     """The entry point on the current stream of device `dev`, with that device current for the call."""
-    if dev == torch.cuda.current_device():
-        _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == torch._C._cuda_getDevice():
+        status = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(dev))
+            status = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise _lib.FAError(status, _lib.load().fa_get_error().decode())
 
 
 @functools.lru_cache(maxsize=4096)
