@@ -15,6 +15,8 @@
 // Bound: HBM, every value read and written once (a launch's latency for single tokens).  A thread
 // takes 16 features of a token (two 16-byte loads: the two halves of its pairs) and walks over heads
 // of that token, so that one read of the tables serves up to 8 heads.
+// Measured (B200, 32/8 heads, d = 128): 8 prompts of up to 2048 tokens 62 us in bf16 (6.0 TB/s, 92 % of the copy rate) and
+// 67 us in e4m3 (5.1 TB/s: its pages wait for the scale, one load after another); 64 single tokens 2.4 and 3.0 us.
 #pragma once
 #include <cuda_bf16.h>
 #include "paged_sm100.cuh"
