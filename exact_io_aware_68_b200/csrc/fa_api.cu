@@ -534,19 +534,21 @@ fa_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, 
   return launch_status(what);
 }
 
-// Warps per row: 8 while that makes at most 4 CTAs per SM (few rows, many partials each), 4 while it
-// makes at most 16, else 1.
+// Warps per row: 8 while that makes at most 4 CTAs per SM (few rows, many partials each), 4 while it makes at most 16,
+// else 1.  Partials in flight per warp: 8, but with 4 warps and at most 8 partials a row on average 2, since idle slots
+// cost (64 ragged sequences with 8 instead of 2: 93.3 against 90 us; 5 drafted tokens with 2 instead of 8: 29.8 against
+// 28.2 us; 1 x 1000 keys with 4 instead of 8: 9.7 against 8.9 us).
 template <int D>
 fa_status launch_paged_combine(const fa::PagedParams& p, int tile_rows, int sms, cudaStream_t s) {
   const long long rows = (long long)p.B * p.Hkv * p.R;
   const char* what = "fa_fwd_paged combine kernel launch";
-  if (rows <= 4LL * sms)
-    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 8>, unsigned(rows), 256, 0, s, what, p, tile_rows);
-  if (rows <= 32LL * sms)
-    return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 4>, unsigned((rows + 1) / 2), 256, 0, s, what, p,
-                                                  tile_rows);
-  return launch_dependent<fa::PagedParams, int>(fa::fa_paged_combine_kernel<D, 1>, unsigned((rows + 7) / 8), 256, 0, s, what, p,
-                                                tile_rows);
+  auto launch = [&](void (*kernel)(fa::PagedParams, int), long long ctas) {
+    return launch_dependent<fa::PagedParams, int>(kernel, unsigned(ctas), 256, 0, s, what, p, tile_rows);
+  };
+  if (rows <= 4LL * sms) return launch(fa::fa_paged_combine_kernel<D, 8, 8>, rows);
+  if (rows > 32LL * sms) return launch(fa::fa_paged_combine_kernel<D, 1, 4>, (rows + 7) / 8);
+  const bool many = (long long)p.n_warps > 8LL * p.B * p.Hkv * p.row_tiles;
+  return launch(many ? fa::fa_paged_combine_kernel<D, 4, 8> : fa::fa_paged_combine_kernel<D, 4, 2>, (rows + 1) / 2);
 }
 
 template <int D, bool FP8, int NG>

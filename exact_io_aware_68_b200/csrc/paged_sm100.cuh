@@ -748,29 +748,45 @@ struct PagedMerge {
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
   }
-  __device__ __forceinline__ void add(float m1, float l1, const float* x) {
-    if (l1 == 0.f) return;   // no key seen there (its m may be -inf)
-    const float mn = fmaxf(m, m1);
-    const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn), c = ex2_approx(m1 - mn);
-    l = l * a + l1 * c;
+  // N partials at once: their maximum first, then all weights side by side.  l1 = 0: no key seen there (m1 may be -inf)
+  template <int N>
+  __device__ __forceinline__ void add(const float (&m1)[N], const float (&l1)[N], const float (&x)[N][PER]) {
+    float mx = m;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = acc[e] * a + x[e] * c;
-    m = mn;
+    for (int u = 0; u < N; ++u) mx = l1[u] != 0.f ? fmaxf(mx, m1[u]) : mx;
+    const float base = mx == -INFINITY ? 0.f : mx;
+    const float a = ex2_approx(m - base);
+    m = mx;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= a;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const bool seen = l1[u] != 0.f;
+      const float c = ex2_approx(m1[u] - base);
+      l += seen ? l1[u] * c : 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] += seen ? x[u][e] * c : 0.f;
+    }
   }
-  // partials sub, sub + step, ... of one row, four in flight; the first partial may be its warp's (CTA's) second slot,
+  // partials sub, sub + step, ... of one row, N in flight; the first partial may be its warp's (CTA's) second slot,
   // the others are the first ones of theirs
+  template <int N>
   __device__ __forceinline__ void gather(const PagedParams& p, int2 info, int sub, int step, int rows, int srow, int lane) {
     const int first = info.x >> 1;
-    for (int w0 = first + sub; w0 <= info.y; w0 += 4 * step) {
-      float2 ml[4];
-      float x[4][PER];
+    for (int w0 = first + sub; w0 <= info.y; w0 += N * step) {
+      float m1[N], l1[N], x[N][PER];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < N; ++u) {
         const int w = w0 + u * step;
-        ml[u] = make_float2(0.f, 0.f);
+        m1[u] = l1[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) x[u][e] = 0.f;
         if (w > info.y) continue;
         const int64_t slot = (int64_t)(w == first ? info.x : 2 * w) * rows + srow;
-        ml[u] = p.part_ml[slot];
+        const float2 ml = p.part_ml[slot];
+        m1[u] = ml.x;
+        l1[u] = ml.y;
         const float* from = p.part_o + slot * (32 * PER) + lane * PER;
         if constexpr (PER == 4) {
           const float4 f = *reinterpret_cast<const float4*>(from);
@@ -780,8 +796,7 @@ struct PagedMerge {
           x[u][0] = f.x; x[u][1] = f.y;
         }
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) add(ml[u].x, ml[u].y, x[u]);
+      add<N>(m1, l1, x);
     }
   }
   __device__ __forceinline__ void store(const PagedParams& p, int64_t row, int lane) const {
@@ -793,10 +808,10 @@ struct PagedMerge {
   }
 };
 
-// Merges the partials of query rows that several warps made, WPR warps of a CTA per row.  Rows of a row
+// Merges the partials of query rows that several warps made, WPR warps of a CTA per row, N partials in flight per warp.  Rows of a row
 // tile that one warp had whole are done already.  Also writes the rows of sequences without keys or
 // without new tokens: O = 0, lse = -inf.
-template <int D, int WPR>
+template <int D, int WPR, int N>
 __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, const int tile_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int PER = D / 32, RPC = 8 / WPR;   // features per lane, rows per CTA
@@ -808,7 +823,7 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
   const int2 info = p.info[(int64_t)bh * p.row_tiles + r / tile_rows];
   const bool whole = has && info.y < 0;
   PagedMerge<PER> a;
-  if (real && has && !whole) a.gather(p, info, sub, WPR, tile_rows, r % tile_rows, lane);
+  if (real && has && !whole) a.template gather<N>(p, info, sub, WPR, tile_rows, r % tile_rows, lane);
   if constexpr (WPR > 1) {
     __shared__ float sm[8], sl[8], so[8][D];
     if (lane == 0) {
@@ -819,8 +834,15 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
     for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = a.acc[e];
     __syncthreads();
     if (sub != 0) return;
+    float m1[WPR - 1], l1[WPR - 1], x[WPR - 1][PER];
 #pragma unroll
-    for (int y = 1; y < WPR; ++y) a.add(sm[warp + y], sl[warp + y], &so[warp + y][lane * PER]);
+    for (int y = 1; y < WPR; ++y) {
+      m1[y - 1] = sm[warp + y];
+      l1[y - 1] = sl[warp + y];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) x[y - 1][e] = so[warp + y][lane * PER + e];
+    }
+    a.template add<WPR - 1>(m1, l1, x);
   }
   if (real && !whole) a.store(p, row, lane);
 }

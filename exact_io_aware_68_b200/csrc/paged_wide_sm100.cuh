@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid
     const int i = (2 * pair + x) * q.tq + r / q.g;
     if (i >= p.Nq) break;
     PagedMerge<D / 32> a;
-    if (has) a.gather(p, info, 0, 1, 256, 128 * x + r, lane);
+    if (has) a.template gather<2>(p, info, 0, 1, 256, 128 * x + r, lane);
     a.store(p, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, lane);
   }
 }
