@@ -81,7 +81,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 __device__ __forceinline__ void load8(const float* src, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  const float4 a = global_load(reinterpret_cast<const float4*>(src)), b = global_load(reinterpret_cast<const float4*>(src) + 1);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
@@ -121,7 +121,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
   }
   int64_t page = -1;
   if (POOL && pos >= 0) {
-    page = __ldg(p.page_table + (int64_t)b * p.max_pages + (pos >> p.page_shift));
+    page = global_load(p.page_table + (int64_t)b * p.max_pages + (pos >> p.page_shift));
     if (page < 0 || page >= p.n_pages) {
       record_status(kStatusRange);
       page = -1;
@@ -139,8 +139,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
       const int which = hh < p.Hq ? 0 : hh < p.Hq + p.Hkv ? 1 : 2;
       const int h = which == 0 ? hh : which == 1 ? hh - p.Hq : hh - p.Hq - p.Hkv;
       const uint4* src = reinterpret_cast<const uint4*>(p.x[which] + b * p.sb[which] + h * p.sh[which] + i * p.sn[which]);
-      w[u].a = __ldg(src + ca);
-      w[u].b = __ldg(src + cb);
+      w[u].a = global_load(src + ca);
+      w[u].b = global_load(src + cb);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) f
   const long long base = (long long)pg << p.page_shift;
   if (base >= L) return;
   const int lo = int(base > start ? base : start), hi = int(base + page_size < L ? base + page_size : L);
-  const int64_t page = __ldg(p.page_table + (int64_t)b * p.max_pages + pg);   // (in flight with the rows)
+  const int64_t page = global_load(p.page_table + (int64_t)b * p.max_pages + pg);   // (in flight with the rows)
   const int old = lo - int(base), m = hi - lo;
 
   const int lpr = p.d / 16, lane = int(threadIdx.x) % lpr, r0 = int(threadIdx.x) / lpr, rpp = THREADS / lpr;
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) f
     const int r = r0 + u * rpp;
     if (r >= m) continue;
     const uint4* row = reinterpret_cast<const uint4*>(src + r * p.sn[1 + kv]);
-    wa[u] = __ldg(row + ca);
-    wb[u] = __ldg(row + cb);
+    wa[u] = global_load(row + ca);
+    wb[u] = global_load(row + cb);
   }
   if (page < 0 || page >= p.n_pages) {
     record_status(kStatusRange);

@@ -70,6 +70,11 @@ struct PagedParams {
   float scale_log2;
 };
 
+// A plain load.  Not __ldg: these kernels start while the one before them on the stream may still write what they read
+// (they wait for it first), and the read-only path wants data that is constant for a kernel's whole life.
+template <typename T>
+__device__ __forceinline__ T global_load(const T* p) { return *p; }
+
 template <int OFF>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {   // 16 bytes from src + OFF
   asm volatile("cp.async.cg.shared.global [%0], [%1 + %2], 16;" :: "r"(dst), "l"(src), "n"(OFF) : "memory");
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
 #pragma unroll
     for (int x = 0; x < G; ++x) {
       const int key = ld.t * KT + 16 * x;
-      ids[x] = key < ld.L ? __ldg(p.page_table + (int64_t)ld.b * p.max_pages + (key >> p.page_shift)) : 0;
+      ids[x] = key < ld.L ? global_load(p.page_table + (int64_t)ld.b * p.max_pages + (key >> p.page_shift)) : 0;
     }
   };
   // A lane copies chunk c of keys r0, r0 + RPI, ... of each group.  RPI is a power of two and r0 below it, so the swizzle

@@ -140,7 +140,7 @@ __device__ __forceinline__ void wide_split_queries(const WideParams& q) {
   const int c = threadIdx.x % LPR;
   for (int64_t row = ((int64_t)(blockIdx.x - 1) * 1024 + threadIdx.x) / LPR; row < (rows + 31) / 32 * 32; row += (int64_t)(gridDim.x - 1) * (1024 / LPR)) {
     const bool real = row < rows;
-    const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(q.p.q + row * D) + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 w = real ? global_load(reinterpret_cast<const uint4*>(q.p.q + row * D) + c) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     float mx = 0.f;
     bool finite = true;
@@ -391,7 +391,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   auto has_piece = [&](const WideSeg& w, int j, int i) { return i < pieces && (w.t + j) * 128 + i * piece_rows < w.L; };
   auto piece_page = [&](const WideSeg& w, int j, int i) -> int {   // its page (not looked at yet)
     const int key = (w.t + j) * 128 + i * piece_rows;
-    const int id = has_piece(w, j, i) ? __ldg(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift)) : 0;
+    const int id = has_piece(w, j, i) ? global_load(p.page_table + (int64_t)w.b * p.max_pages + (key >> p.page_shift)) : 0;
     return id;
   };
 
@@ -674,11 +674,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // one block ahead, its page two blocks
       auto group_page = [&](int j) -> int {
         const int key = (s.t + j) * 128 + 16 * (ct & 7);
-        return ct < 16 && j < n_max && key < s.L ? __ldg(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
+        return ct < 16 && j < n_max && key < s.L ? global_load(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
       };
       auto group_scale = [&](int id) -> float {
         if (unsigned(id) >= unsigned(p.n_pages)) return ct < 8 ? 1.f : 0.f;
-        return __ldg((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
+        return global_load((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
       };
       float next_scale = group_scale(group_page(0));
       int next_id = group_page(1);
