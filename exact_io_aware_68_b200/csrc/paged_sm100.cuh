@@ -27,12 +27,13 @@
 //    fa_paged_combine_kernel.
 //  * 12 warps of 168 registers with two tiles of 8 KB each in their rings for 8 rows, 8 warps with three beyond: what
 //    spills nothing (shared memory takes nearly all of L1, so a spilled register is a trip to L2).
-// Measured (B200, the whole call, 32/8 heads, D = 128): 64 sequences of 100 to 4000 keys, one query each, 90 us in bf16
-// (6.0 TB/s of K and V, 91 % of the copy rate) and 57 us in e4m3 (4.7 TB/s; there the warps' own latency bounds:
+// Measured (B200, the whole call, 32/8 heads, D = 128): 64 sequences of 100 to 4000 keys, one query each, 89 us in bf16
+// (6.05 TB/s of K and V, 92 % of the copy rate) and 56 us in e4m3 (4.8 TB/s; there the warps' own latency bounds:
 // issue slots 44 % used, waits on memory rare); 16 heads x 65,536 keys, 8 queries, 91 us (5.9 TB/s); 8 x 32,768 keys
 // e4m3, 64/8 heads, 93 us (5.8 TB/s).  About 10 us of a call are launch, look-ups, first loads and the merge.
 // Tried and slower: tiles of 2 KB with 14 to 16 warps (57 -> 60 us e4m3), a loop over 16-key groups in place of unrolled
-// tiles (57 -> 58 us), a 16-row tile with untransposed products (102 us e4m3).
+// tiles (57 -> 58 us), a 16-row tile with untransposed products (102 us e4m3), S by 8-bit MMAs with queries of two 8-bit parts
+// (56 -> 59 us; 20 rows, D = 64: 28 -> 36 us, registers spill).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -17,8 +17,8 @@
 //    is turned into f16 (exact; NaN stays NaN) by four more warps, in the swizzled layout the MMA reads.  The
 //    page's key scale multiplies the finished scores, its value scale the probabilities.
 // Measured (B200, the whole call): 4 sequences, 512 new tokens against 4097 to 8100 keys, 32/8 heads, D = 128, causal:
-// 187 us in bf16 (990 TFLOP/s, 0.61 of the measured cuBLAS burst rate; tensor pipe active 56 %, as in the training
-// forward: the chain S, softmax, PV of the tiles bounds), 3 x 256 new tokens in e4m3 103 us (625 TFLOP/s; tensor
+// 184 us in bf16 (1010 TFLOP/s, 0.62 of the measured cuBLAS burst rate; tensor pipe active 56 %, as in the training
+// forward: the chain S, softmax, PV of the tiles bounds), 3 x 256 new tokens in e4m3 102 us (630 TFLOP/s; tensor
 // pipe 37 %).  A clock trace of the latter shows 4200 cycles a unit in the steady state (bf16: 3750) and about 10,000 at
 // every change of segment, where code that has left the instruction cache runs: hence the rolled loops there.
 // Tried and slower: both tiles on alternating key blocks of one 128-row tile (75 -> 81 us for 64 rows, bf16); V and K both
