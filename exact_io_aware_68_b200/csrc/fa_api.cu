@@ -660,6 +660,9 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   FA_CHECK_PTR(lse);
   FA_CHECK_PTR(page_table);
   FA_CHECK_PTR(key_lens);
+  // (rows of q are read again after others' o is there, where a pair is computed anew)
+  const uint64_t at_q = reinterpret_cast<uintptr_t>(q), at_o = reinterpret_cast<uintptr_t>(o), bytes = uint64_t(B) * Hq * Nq * d * 2;
+  if ((at_o > at_q ? at_o - at_q : at_q - at_o) < bytes) return fail(FA_ERR_INVALID_ARG, "o overlaps q");
   if (fp8) {
     FA_CHECK_PTR(k_scale);
     FA_CHECK_PTR(v_scale);

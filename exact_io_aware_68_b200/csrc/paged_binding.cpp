@@ -1,5 +1,5 @@
 // Compiled argument marshalling for paged.py: the checks, the allocations and the call of kv_append and
-// attention_paged, which in Python cost 15 us a call, more than a decode step's kernels.  Only the path of a call
+// attention_paged, which in Python cost 11 (attention) to 13 us (append) of a call, more than a decode step's kernels.  Only the path of a call
 // that fits is here: anything else returns None, and paged.py says what does not fit.  No CUDA code; the work is the
 // C ABI's (libfa_sm100.so).
 #include <Python.h>
@@ -41,7 +41,7 @@ struct Cache {
   bool fp8;
 };
 
-// What _cache_fits of paged.py checks.
+// What _refuse_cache of paged.py names the faults of.
 bool cache_fits(const Tensor& k, const Tensor& v, const Arg& ks, const Arg& vs, const Tensor& table, const Tensor& lens, const Arg& news,
                 int64_t B, int64_t d, Cache& c) {
   if (!k.is_cuda() || !v.is_cuda() || k.dim() != 4 || k.size(3) != d || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type())

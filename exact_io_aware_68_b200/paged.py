@@ -9,7 +9,7 @@ its new ones, so that one step is
     o, lse = attention_paged(q, k_cache, v_cache, page_table, key_lens, causal=True, new_lens=new_lens)
 
 Both calls run on the current stream of the pools' device, and can be captured into a CUDA graph whose
-replays read the lengths and the table anew.
+replays read the lengths and the table anew.  They are for serving: no gradient flows through them.
 """
 import functools
 
@@ -84,7 +84,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, key_lens, new_lens=None, rope=
     k, v: bf16 [B, Hkv, Nq, d]; q: bf16 [B, Hq, Nq, d] or None; any strides that are multiples of 8 with d
     contiguous (views of a projection's output need no copy).  rope: (cos, sin) tables, applied to k and q by position
     (``rope_tables``); interleaved: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Writes the pools (and
-    the scales of e4m3 pools) in place; returns the rotated queries, contiguous [B, Hq, Nq, d], or None."""
+    the scales of e4m3 pools) in place; returns the rotated queries, contiguous [B, Hq, Nq, d], or None.  q_out: where
+    to write those; a contiguous q itself, or no memory of q's."""
     cos, sin = (None, None) if rope is None else rope
     out = _binding().append(k, v, k_cache, v_cache, page_table, key_lens, new_lens, cos, sin, interleaved, q, k_scale, v_scale, q_out)
     if out is True:
@@ -107,6 +108,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, key_lens, new_lens=None, rope=
         _need(t.device == device, f"{name} is on {t.device}, k_cache on {device}")
         _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
         _need(t.stride(3) == 1, f"{name} must be contiguous in its last dimension")
+    _need((cos is None) == (sin is None), "rope needs both tables, (cos, sin)")
     for name, t in (("rope cos", cos), ("rope sin", sin)):
         _need(t is None or (t.dim() == 2 and t.dtype == torch.float32 and t.is_contiguous() and t.device == device and t.shape == cos.shape),
               f"{name} must be contiguous fp32 [max_pos, rot / 2] on {device}, cos and sin alike")
@@ -129,7 +131,8 @@ def attention_paged(q, k_cache, v_cache, page_table, key_lens, scale=None, causa
     ``fa_fwd_paged_e4m3``).
 
     q: bf16 [B, Hq, Nq, d] contiguous, Hq a multiple of the pools' Hkv.  Query i of sequence b stands at position
-    key_lens[b] - new_lens[b] + i; causal keeps the keys up to it.  Queries i >= new_lens[b] get O = 0, lse = -inf."""
+    key_lens[b] - new_lens[b] + i; causal keeps the keys up to it.  Queries i >= new_lens[b] get O = 0, lse = -inf.
+    o must not overlap q."""
     out = _binding().attention(q, k_cache, v_cache, page_table, key_lens, new_lens, k_scale, v_scale, workspace, o, lse, scale, causal)
     if type(out) is tuple:
         return out

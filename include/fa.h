@@ -189,7 +189,7 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  *    i of sequence b stands at position key_lens[b] - new_lens[b] + i.  The same two arrays go to the
  *    append and to the attention.
  *  - Grouped heads: query head h uses K/V head h / (Hq / Hkv); Hq must be a multiple of Hkv.
- *  - 1 <= B <= 4096, B * Hq <= 65535, and B * max_pages * page_size < 2^31.
+ *  - 1 <= B <= 4096, B * Hq <= 65535, Nq <= 2^20, and B * max_pages * page_size < 2^31.
  *  - What the device finds out of range (a page number outside [0, n_pages), key_lens outside
  *    [0, max_pages * page_size], new_lens outside [0, Nq], an append before position 0 or past the
  *    rotation tables) is not accessed; fa_check() then returns FA_ERR_RANGE, and the outputs of
@@ -199,8 +199,8 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
 /* Appends the new keys and values to the pool, rotating keys (and queries) by their positions.
  * q, k, v: bf16 [B, Hq | Hkv | Hkv, Nq, d] with d contiguous; strides: HOST array of nine element strides
  * (batch, head, token of q, then k, then v), multiples of 8, so that views of one projection output need
- * no copy.  q may be NULL (then q_out is not written); q_out: bf16 [B, Hq, Nq, d] contiguous, rows of
- * queries that are no token (i >= new_lens[b]) are set to 0.  Rows of the pool that get no token keep
+ * no copy.  q may be NULL (then q_out is not written); q_out: bf16 [B, Hq, Nq, d] contiguous (a contiguous q
+ * itself, or without overlap), rows of queries that are no token (i >= new_lens[b]) are set to 0.  Rows of the pool that get no token keep
  * their bytes.
  * Rotation: rope_cos, rope_sin fp32 [max_pos, rot_dim / 2], both NULL for none; rot_dim a multiple of
  * 16, at most d; features past rot_dim pass through.  Pair (x, y) becomes (x cos - y sin,
@@ -229,7 +229,8 @@ FA_API fa_status fa_kv_append_e4m3(const void* q, const void* k, const void* v, 
 
 /* Attention of Nq >= 1 new queries per head to the keys of their sequences in the pool: single tokens,
  * drafted tokens, chunks of prompts and whole prompts.
- * q: bf16 [B, Hq, Nq, d] contiguous; writes o (bf16, the same shape) and lse (fp32 [B, Hq, Nq]).  Query i
+ * q: bf16 [B, Hq, Nq, d] contiguous, B * Hq * Nq < 2^31; writes o (bf16, the same shape, refused where it
+ * overlaps q) and lse (fp32 [B, Hq, Nq]).  Query i
  * of sequence b sees keys j < key_lens[b], and with causal != 0 only j <= key_lens[b] - new_lens[b] + i.
  * A query with no key, and one that is no token (i >= new_lens[b]), gets O = 0 and lse = -inf.
  * workspace: at least fa_fwd_paged_workspace_size() bytes (of the current device; with no visible

@@ -656,6 +656,37 @@ def test_append_refuses_on_the_host(over, status, fp8):
     assert c_append(lib, fp8, **over) == status and lib.fa_get_error()
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_attention_refuses_o_over_q(fp8):
+    build()
+    lib = _lib.load()
+    n = 2 * 64 * 2   # bytes of q and of o
+    for o in (FAKE, FAKE + n - 16, FAKE - n + 16):
+        assert c_attention(lib, fp8, o=o) == INV and b"overlaps" in lib.fa_get_error()
+    for o in (FAKE + n, FAKE - n):   # side by side: refused for the next reason only
+        assert c_attention(lib, fp8, o=o, ws=0) == INV and b"workspace" in lib.fa_get_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_rotates_a_contiguous_q_in_place(fp8, interleaved):
+    g = torch.Generator().manual_seed(11)
+    B, Hq, Hkv, Nq, d = 3, 6, 2, 5, 128
+    q = bf16(torch.randn((B, Hq, Nq, d), generator=g)).cuda()
+    k, v = (bf16(torch.randn((B, Hkv, Nq, d), generator=g)).cuda() for _ in range(2))
+    rope = fa.rope_tables(64, 96)
+    outs = []
+    for in_place in (False, True):
+        c = Cache(B, Hkv, d, 16, [40, 5, 17], fp8, seed=3)
+        x = q.clone()
+        y = fa.kv_append(k, v, *c.args(), i32([40, 5, 17]), i32([5, 5, 2]), rope=rope, interleaved=interleaved, q=x, **c.scales(),
+                         q_out=x if in_place else None)
+        assert (y is x) == in_place
+        outs.append((y, *(t.view(torch.uint8) for t in c.args()[:2])))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and not outs[1][0][2, :, 2:].any()
+
+
 @pytest.mark.parametrize("missing", ["ks", "vs"])
 def test_e4m3_needs_scales(missing):
     build()
