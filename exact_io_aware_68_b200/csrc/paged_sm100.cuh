@@ -25,8 +25,11 @@
 //    whatever the lengths are, nothing depends on the longest sequence, and the workspace (two partials per
 //    warp) depends on the device alone.  A row tile that several warps shared is merged by
 //    fa_paged_combine_kernel.
-//  * 12 warps of 168 registers with two tiles of 8 KB each in their rings for 8 rows, 8 warps with three beyond: what
-//    spills nothing (shared memory takes nearly all of L1, so a spilled register is a trip to L2).
+//  * 12 warps of 168 registers for 8 rows, 8 warps of 255 beyond, with rings of two tiles of 8 KB: what spills least.  Shared
+//    memory is taken from L1, and where it takes nearly all of it a spilled register is a trip to L2: a third tile
+//    costs 20 rows of D = 128 48.2 against 45.3 us in bf16, and gains nothing elsewhere (16 rows 58.2 against 57.7).
+//    Tiles of 4 KB where an e4m3 tile's scores would not fit into the registers beside O: 32 rows of D = 64 39.4 -> 33.0 us,
+//    24 of D = 128 49.3 -> 45.2 us (16 rows, where they fit, 48 -> 56 us).
 // Measured (B200, the whole call, 32/8 heads, D = 128): 64 sequences of 100 to 4000 keys, one query each, 89 us in bf16
 // (6.05 TB/s of K and V, 92 % of the copy rate) and 56 us in e4m3 (4.8 TB/s; there the warps' own latency bounds:
 // issue slots 44 % used, waits on memory rare); 16 heads x 65,536 keys, 8 queries, 91 us (5.9 TB/s); 8 x 32,768 keys
@@ -173,12 +176,12 @@ __device__ __forceinline__ long long paged_share(long long W, int i, int n) {
 template <int D, bool FP8, int NG>
 struct PagedLayout {
   static constexpr int ROWB = FP8 ? D : 2 * D;         // bytes of one key
-  static constexpr int TILE = 4096;                    // bytes of a tile's K, and of its V
+  static constexpr int TILE = FP8 && (NG == 4 || (NG == 3 && D == 128)) ? 2048 : 4096;   // bytes of a tile's K, and of its V
   static constexpr int KT = TILE / ROWB;               // keys per tile: 16, 32 or 64
   static constexpr int GROUPS = KT / 16;               // 16-key groups: each inside one page
   static constexpr int CPR = ROWB / 16;                // 16-byte chunks per key
   static constexpr int WARPS = NG == 1 ? 12 : 8;
-  static constexpr int STAGES = NG == 1 ? 2 : 3;
+  static constexpr int STAGES = 2;
   static constexpr int STAGE = 2 * TILE + (FP8 ? 128 : 0);   // K, V, and the groups' scales
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int bytes(int B) { return RING + (B + 1) * 4; }
