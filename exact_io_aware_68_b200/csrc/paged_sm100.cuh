@@ -10,7 +10,7 @@
 // Mathematics (the online softmax of the other kernels): s = tau q.k, running reference max m and
 // sum l, O = sum 2^(s' - m) v with s' = s log2 e; partials of one row over disjoint keys merge by
 // m* = max m_i, O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.  With e4m3 pages k = c * ks, where
-// ks is constant over a page, so ks multiplies the finished dot product and vs the probability.
+// ks is constant over a page, so ks multiplies the finished dot product and vs the probability (or V, see PagedUnit).
 //
 // Bound: HBM.  A key and its value are 4 D bytes (2 D in e4m3) for 4 D flop per row: at most 32
 // flop per byte for 16 rows.  Each SM gets 23 bytes a cycle of the measured copy rate, i.e. 16 keys
@@ -49,6 +49,38 @@ enum : int { kStatusRange = 6 };   // a page number, length or position outside 
 constexpr int kPagedMaxB = 4096;   // the prefix of the tile counts sits in shared memory
 constexpr float kPagedRescale = 8.0f;   // the reference max moves only when a tile exceeds it by 2^8
 constexpr float kPagedPScale = 128.0f;  // e4m3: probabilities enter the f16 MMA times 2^7 (at most 2^15)
+constexpr float kPagedLeastUnit = 6.0185311e-36f;   // 2^-117, the least scale that the append gives
+constexpr float kPagedFarUnit = 1.0995116e12f;      // 2^40
+
+// Value scales of one row tile's stretch of keys, e4m3.  O is kept in units of `unit` / 2^7, and P enters the f16 product as
+// p s 2^7 / unit, at most 2^15 where s <= unit.  But f16 ends at 2^-24: with the largest scale so far as the unit, a page 2^21
+// below it loses bits and one 2^32 below it everything, also in rows that do not see the loud page, or see nothing but
+// zeros in it.  So f16 is for scales within 2^8 of one another (it then loses 2^-24 of a page's own unit).  From the first scale
+// on that lies further away the stretch is `far`: P enters as bf16 without the scale, V as bf16 times its scale (exact where
+// that is a power of two), in units that leave room at both ends, 2^40 (O: up to 2^128, full precision down to 2^-93).
+// That takes 2 to 3 times as long in the narrow kernels (64 ragged sequences 56 -> 159 us) and as long as ever in the wide one;
+// to be ready for it costs calls that never meet it 1 to 2 % (32 rows of D = 64 33.0 -> 34.9 us, whole prompts 220 -> 228).
+struct PagedUnit {
+  float unit, least;   // least: of the scales so far; 0: far
+  __device__ __forceinline__ void reset() {
+    unit = kPagedLeastUnit;
+    least = INFINITY;
+  }
+  __device__ __forceinline__ bool far() const { return least == 0.f; }
+  // hi, lo: the largest and least scale of more pages.  True where the unit changed; O times `move` is what it was.
+  __device__ __forceinline__ bool meet(float hi, float lo, float& move) {
+    if ((hi <= unit && lo >= least) || far()) return false;
+    const float was = unit;
+    unit = fmaxf(unit, hi);
+    least = fminf(least, lo);
+    if (unit > 256.f * least) {
+      unit = kPagedFarUnit;
+      least = 0.f;
+    }
+    move = was / unit;
+    return unit != was;
+  }
+};
 constexpr float kPagedLn2 = 0.69314718055994530942f;
 
 struct PagedParams {
@@ -140,6 +172,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// two f16 times s as bf16x2
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t w, float s) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16x2(f.x * s, f.y * s);
 }
 
 // Nonzero where one of the values in w (two bf16 or four e4m3) is not finite.
@@ -356,7 +394,9 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
   float o[NG][C][4];
   float m[NG][2], l[NG][2], sc[NG][2];   // rows 2 t4 + i; sc: score scale in the log2 domain
   int lim[NG][2], limg[NG], lim_lo;      // keys < lim allowed; limg: of row g; lim_lo: the smallest that is not zero
-  float vref = 0.f, unit = 0.f;          // e4m3: the largest value scale so far, O is in units of it; kPagedPScale / vref
+  PagedUnit vu;                          // e4m3: the units of O
+  vu.reset();
+  float unit = 0.f;                      // kPagedPScale / vu.unit
   int stage = 0;
   bool fresh = true;
   long long seg = w0;                    // first tile of the running segment
@@ -419,8 +459,8 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
           for (int e = 0; e < 4; ++e) o[ng][c][e] = 0.f;
       }
       lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
-      vref = 6.0185311e-36f;   // 2^-117
-      unit = kPagedPScale / vref;
+      vu.reset();
+      unit = kPagedPScale / vu.unit;
     }
 
     // ---- the next tile of the list goes into the stage that the previous iteration emptied
@@ -521,13 +561,14 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
         over |= alpha[ng][i] > m[ng][i] + kPagedRescale;
       }
     if constexpr (FP8) {
-      float vmax = vref;
+      float hi = 0.f, lo = INFINITY;   // (groups past the end have scale 0)
 #pragma unroll
-      for (int x = 0; x < G; ++x) vmax = fmaxf(vmax, vsc[x]);
-      if (vmax > vref) {   // the same in every lane
-        vmove = vref / vmax;
-        vref = vmax;
-        unit = kPagedPScale / vref;
+      for (int x = 0; x < G; ++x) {
+        hi = fmaxf(hi, vsc[x]);
+        lo = vsc[x] > 0.f ? fminf(lo, vsc[x]) : lo;
+      }
+      if (vu.meet(hi, lo, vmove)) {   // the same in every lane
+        unit = kPagedPScale / vu.unit;
         over = true;
       }
 #pragma unroll
@@ -555,10 +596,11 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
           for (int e = 0; e < 4; ++e) o[ng][c][e] *= alpha[ng][e & 1];
       }
     }
-    // P^T as operand columns; 16-bit parts: f16 (e4m3, times the page's value scale), else bf16 in two parts
-    // for up to 8 rows: the product is not what bounds the kernel, and P then has 16 bits
+    // P^T as operand columns; 16-bit parts: f16 (e4m3, times the page's value scale; bf16 where scales lie far apart), else
+    // bf16 in two parts for up to 8 rows: the product is not what bounds the kernel, and P then has 16 bits
     constexpr bool LOW = !FP8 && NG == 1;
     uint32_t pf[G][NG][2], pl[LOW ? G : 1][2];
+    const bool far = FP8 && vu.far();
 #pragma unroll
     for (int ng = 0; ng < NG; ++ng) {
       const float n0 = m[ng][0] == -INFINITY ? 0.f : -m[ng][0], n1 = m[ng][1] == -INFINITY ? 0.f : -m[ng][1];
@@ -570,7 +612,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
           l[ng][0] += p0;
           l[ng][1] += p1;
           if constexpr (FP8) {
-            pf[x][ng][y] = movmatrix_trans(pack_f16x2(p0 * vsc[x], p1 * vsc[x]));
+            pf[x][ng][y] = movmatrix_trans(far ? pack_bf16x2(p0, p1) : pack_f16x2(p0 * vsc[x], p1 * vsc[x]));
           } else {
             const uint32_t hi = pack_bf16x2(p0, p1);
             pf[x][ng][y] = movmatrix_trans(hi);
@@ -582,7 +624,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
 
     // ---- O^T += V^T P^T.  A value that is not finite must not reach a row that does not see its key (0 * inf):
     // where rows see different keys of the tile and such a value is there, it is taken out of the
-    // product and its effect is added to the rows that do see it.
+    // product and its effect is added to the rows that do see it.  That, and scales far apart, in a loop of little code.
     bool careful = false;
     if (lim_lo < min(cp.L, k0 + KT)) {
       uint32_t bad = 0;
@@ -610,7 +652,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
       }
     };
     constexpr int PER = FP8 ? 2 : 1;   // feature blocks per ldmatrix
-    if (!careful) {
+    if (!careful && !far) {
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         constexpr int BATCH = C / PER < 4 ? C / PER : 4;
@@ -637,6 +679,12 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
 #pragma unroll 1
       for (int x = 0; x < G; ++x) {
         uint32_t see[NG][2], px[NG][2], plx[2] = {0u, 0u};   // see: 1 where row g sees the key
+        float vx = 0.f;                                      // the group's value scale in units of O
+        if constexpr (FP8) {
+#pragma unroll
+          for (int z = 0; z < G; ++z)
+            if (z == x) vx = vsc[z];
+        }
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -666,17 +714,26 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
               for (int q = 0; q < 2; ++q) {
                 const uint32_t v = (a[e] >> (16 * q)) & 0xffffu;
                 const bool special = (v & kExp) == kExp, nan = special && (v & ~kExp & 0x7fffu) != 0;
-                if (!special) keep |= 0xffffu << (16 * q);
-                if (nan || (special && !(v & 0x8000u))) up[e] |= kOne << (16 * q);
-                if (nan || (special && (v & 0x8000u))) dn[e] |= kOne << (16 * q);
+                if (!special || !careful) keep |= 0xffffu << (16 * q);
+                if (careful && (nan || (special && !(v & 0x8000u)))) up[e] |= kOne << (16 * q);
+                if (careful && (nan || (special && (v & 0x8000u)))) dn[e] |= kOne << (16 * q);
               }
               a[e] &= keep;
+            }
+            uint32_t b[4];   // far: the values in bf16, and no f16 product
+            if constexpr (FP8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                b[e] = far ? scaled_bf16x2(a[e], vx) : 0u;
+                a[e] = far ? 0u : a[e];
+              }
             }
             const int c = PER * cc + z;
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng) {
               float cu[4] = {0.f, 0.f, 0.f, 0.f}, cd[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<FP8>(o[ng][c], a[0], a[1], a[2], a[3], px[ng][0], px[ng][1]);
+              mma16816<FP8>(o[ng][c], a[0], a[1], a[2], a[3], far ? 0u : px[ng][0], far ? 0u : px[ng][1]);
+              if constexpr (FP8) mma16816<false>(o[ng][c], b[0], b[1], b[2], b[3], far ? px[ng][0] : 0u, far ? px[ng][1] : 0u);
               if constexpr (LOW) mma16816<false>(o[0][c], a[0], a[1], a[2], a[3], plx[0], plx[1]);
               mma16816<FP8>(cu, up[0], up[1], up[2], up[3], see[ng][0], see[ng][1]);
               mma16816<FP8>(cd, dn[0], dn[1], dn[2], dn[3], see[ng][0], see[ng][1]);
@@ -712,7 +769,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
           if (rt * RT + row >= p.R) continue;
           const bool dead = lim[ng][i] == 0;
           if (dead) lr = 0.f;
-          const float f = (FP8 ? vref * (1.f / kPagedPScale) : 1.f) * (whole ? (lr != 0.f ? 1.f / lr : 0.f) : 1.f);
+          const float f = (FP8 ? vu.unit * (1.f / kPagedPScale) : 1.f) * (whole ? (lr != 0.f ? 1.f / lr : 0.f) : 1.f);
           const int64_t out = (int64_t)(cp.b * p.Hkv + h) * p.R + rt * RT + row;
           const int64_t slot = (2 * (int64_t)me + (seg == w0 ? 0 : 1)) * RT + row;
 #pragma unroll

@@ -15,7 +15,8 @@
 //  * e4m3.  K enters the tensor core as it is: each query row, times a power of two, is split into an e4m3 and an
 //    e5m2 part (8 bits fit into 4 + 3, see below), and S is the sum of two 8-bit products.  P needs 16 bits, so V
 //    is turned into f16 (exact; NaN stays NaN) by four more warps, in the swizzled layout the MMA reads.  The
-//    page's key scale multiplies the finished scores, its value scale the probabilities.
+//    page's key scale multiplies the finished scores, its value scale the probabilities; where value scales lie far apart
+//    (PagedUnit) a block's P and V are bf16, with V times its scale.
 // Measured (B200, the whole call): 4 sequences, 512 new tokens against 4097 to 8100 keys, 32/8 heads, D = 128, causal:
 // 184 us in bf16 (1010 TFLOP/s, 0.62 of the measured cuBLAS burst rate; tensor pipe active 56 %, as in the training
 // forward: the chain S, softmax, PV of the tiles bounds), 3 x 256 new tokens in e4m3 102 us (630 TFLOP/s; tensor
@@ -58,13 +59,14 @@ struct WideLayout {
   static constexpr int VST = (D == 128) ? 2 : 4;
   static constexpr int RST = FP8 ? (D == 128 ? 2 : 4) : 0;   // raw V tiles
   static constexpr int SST = 4;                    // scale sets (one per block)
+  static constexpr int SET = 80;                   // bytes of one: 8 K scales, 8 V scales / unit of P, the unit, far
   static constexpr int QA_OFF = 0;                 // (e4m3: each query tile is two 8-bit tiles)
   static constexpr int QB_OFF = QA_OFF + TILE;
   static constexpr int K_OFF = QB_OFF + TILE;
   static constexpr int V_OFF = K_OFF + KST * KTILE;
   static constexpr int RAW_OFF = V_OFF + VST * TILE;
-  static constexpr int SC_OFF = RAW_OFF + RST * RAW;            // [SST][2][8] fp32: K and V scales of the 16-key groups
-  static constexpr int BAR_OFF = SC_OFF + (FP8 ? SST * 64 : 0);
+  static constexpr int SC_OFF = RAW_OFF + RST * RAW;
+  static constexpr int BAR_OFF = SC_OFF + (FP8 ? SST * SET : 0);
   // q_full[2], q_empty[2], k_full, k_empty, v_full, v_empty, raw_full, raw_empty, s_full[2], p_full[2][2], o_fin[2],
   // o_free[2], tail, fin, seg_full, seg_empty, sc_full
   static constexpr int SEGS = 4;                   // segments scheduled ahead
@@ -558,6 +560,12 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int j = -1; ok && j < n_max; ++j) {
             const int vst = (gk + j) % VST, kst1 = (gk + j + 1) % KST;
             if (j >= 0 && !wait(&v_full[vst], ((gk + j) / VST) & 1)) { ok = false; break; }
+            uint32_t id_pv = kIdPV;
+            if (j >= 0) {   // far: bf16
+              uint32_t far;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(far) : "r"(smem_u32(smem) + L::SC_OFF + (gk + j) % L::SST * L::SET + 68) : "memory");
+              if (far) id_pv |= kType;
+            }
             bool have_k = false;   // K_{j+1} resident
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
@@ -574,7 +582,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
                     mma_ts_elect(tmem + L::o_col(x), tmem + L::s_col(x) + 32 * h + k * 8,
-                                 sdesc_join(v_lo + (4 * h + k) * (2048 >> 4), kHi), kIdPV, (j > 0 || h + k > 0) ? 1u : 0u);
+                                 sdesc_join(v_lo + (4 * h + k) * (2048 >> 4), kHi), id_pv, (j > 0 || h + k > 0) ? 1u : 0u);
                 }
                 if (!ok) break;
               } else if (!wait(&q_full[x], n_i & 1)) {
@@ -662,7 +670,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       __syncwarp();
     }
   } else if (FP8 && warp >= 12) {
-    // =========================================================== converters: V to f16
+    // =========================================================== converters: V to f16, or (far) to bf16 times its scale
     set_regs_dec<L::CVT_REGS>();
     const int ct = tid - 384;
     float* scales = reinterpret_cast<float*>(smem + L::SC_OFF);
@@ -670,37 +678,49 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     bool ok = true;
     while (ok && next_seg(s)) {
       const int n_max = s.cnt;
-      // threads 0-15: K and V scale of 16-key group ct & 7 (past the end 1 and 0: its scores are masked), looked up
-      // one block ahead, its page two blocks
+      // lanes 8-15 of each warp: V scale of 16-key group lane & 7 (past the end 0), lanes 0-7 of the first K's (1: its scores
+      // are masked), looked up one block ahead, their pages two blocks
       auto group_page = [&](int j) -> int {
-        const int key = (s.t + j) * 128 + 16 * (ct & 7);
-        return ct < 16 && j < n_max && key < s.L ? global_load(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
+        const int key = (s.t + j) * 128 + 16 * (lane & 7);
+        return lane < 16 && (warp == 12 || lane >= 8) && j < n_max && key < s.L ? global_load(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
       };
       auto group_scale = [&](int id) -> float {
-        if (unsigned(id) >= unsigned(p.n_pages)) return ct < 8 ? 1.f : 0.f;
-        return global_load((ct < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
+        if (unsigned(id) >= unsigned(p.n_pages)) return lane < 8 ? 1.f : 0.f;
+        return global_load((lane < 8 ? p.k_scale : p.v_scale) + (int64_t)id * p.Hkv + s.h);
       };
       float next_scale = group_scale(group_page(0));
       int next_id = group_page(1);
+      PagedUnit vu;   // the segment's units of O, by each warp for itself
+      vu.reset();
+      float unit = 0.f;   // kPagedPScale / vu.unit
       for (int j = 0; j < n_max; ++j, ++gb) {
         const int key0 = (s.t + j) * 128;
         const int st = gb % RST, dst_st = gb % VST;
-        const float my_scale = next_scale;
+        float my_scale = next_scale;
         next_scale = group_scale(next_id);
         next_id = group_page(j + 2);
+        const bool value = lane >= 8 && my_scale > 0.f;
+        if (__any_sync(0xffffffffu, value && (my_scale > vu.unit || my_scale < vu.least))) {
+          const uint32_t bits = __float_as_uint(my_scale);   // (positive floats order as their bits do)
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, value ? bits : 0u), lo = __reduce_min_sync(0xffffffffu, value ? bits : 0x7f800000u);
+          float move;
+          vu.meet(__uint_as_float(hi), __uint_as_float(lo), move);
+          unit = kPagedPScale / vu.unit;
+        }
+        if (lane >= 8) my_scale *= unit;
         if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[st], (gb / RST) & 1, wc))) { ok = false; break; }
         constexpr int CPR = D / 16;   // raw 16-byte chunks per key, and chunks per thread
         const uint8_t* raw = smem + L::RAW_OFF + st * L::RAW;
         // (a free stage also means that block gb - VST is done with: its scales, SST blocks back, too)
         if (!__all_sync(0xffffffffu, gb < VST || mbar_wait(&v_empty[dst_st], ((gb / VST) - 1) & 1, wc))) { ok = false; break; }
         if (warp == 12) {
-          if (ct < 16) scales[(gb % L::SST) * 16 + ct] = my_scale;
+          const float out = lane < 16 ? my_scale : lane == 16 ? vu.unit : __int_as_float(vu.far());
+          if (lane < 18) scales[(gb % L::SST) * (L::SET / 4) + lane] = out;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[gb % L::SST]);
         }
         uint8_t* dst = smem + L::V_OFF + dst_st * L::TILE;
-#pragma unroll 4
-        for (int i = 0; i < CPR; ++i) {
+        auto convert = [&](int i, auto far_) {
           const int id = i * 128 + ct, row = id / CPR, c = id % CPR;
           const uint4 w = *reinterpret_cast<const uint4*>(raw + id * 16);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -709,6 +729,11 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int e = 0; e < 4; ++e) {
             o[2 * e] = e4m3x2_to_f16x2(u[e]);
             o[2 * e + 1] = e4m3x2_to_f16x2(u[e] >> 16);
+          }
+          if constexpr (decltype(far_)::value) {
+            const float vs = __shfl_sync(0xffffffffu, my_scale, 8 + (row >> 4));   // (a warp's rows are of one group)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = scaled_bf16x2(o[e], vs);
           }
           if (key0 + row >= s.L) {   // past the end: what lies there is nobody's
 #pragma unroll
@@ -722,6 +747,13 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
           *reinterpret_cast<uint4*>(d + (ca << 4)) = z ? second : first;
           *reinterpret_cast<uint4*>(d + (cb << 4)) = z ? first : second;
+        };
+        if (!vu.far()) {
+#pragma unroll 4
+          for (int i = 0; i < CPR; ++i) convert(i, Int<0>());
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < CPR; ++i) convert(i, Int<1>());
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -762,7 +794,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const float sl2 = FP8 ? row_scale : p.scale_log2;
       float m_ref = -INFINITY;   // reference max, exp2 domain
       float l = 0.f;
-      float vref = 6.0185311e-36f;   // e4m3: the largest value scale so far (2^-117), O is in units of it
+      float vref = kPagedLeastUnit;   // e4m3: O is in units of this / 2^7
       for (int j = 0; j < n; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], (nb + j) & 1, wc))) { ok = false; break; }
         tc_fence_after();
@@ -813,10 +845,10 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         };
         if constexpr (FP8) {
           // The scores are read twice, 64 at a time (registers and instruction cache are short here).  sc: K's scales
-          // of the block's 8 groups of 16 keys, then V's.
+          // of the block's 8 groups of 16 keys, then what P takes of V's, then the units of O and whether scales are far apart.
           const int b = gb + j;
           if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[b % L::SST], (b / L::SST) & 1, wc))) { ok = false; break; }
-          const uint32_t sc = smem_u32(smem) + L::SC_OFF + (b % L::SST) * 64;
+          const uint32_t sc = smem_u32(smem) + L::SC_OFF + (b % L::SST) * L::SET;
           auto scales4 = [&](int at, float (&f)[4]) {
             asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(sc + 4 * at));
           };
@@ -827,17 +859,15 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
             reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
           };
-          float vmax = vref, m_cand = -INFINITY;
+          float m_cand = -INFINITY;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             uint32_t sr[64];
-            float ks[4], vs[4];
+            float ks[4];
             scales4(4 * h, ks);
-            scales4(8 + 4 * h, vs);
             load64(h, sr);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              vmax = fmaxf(vmax, vs[u]);
               float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
               for (int c = 16 * u; c < 16 * u + 16; c += 4) {
@@ -850,11 +880,13 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const float neg = move_max(m_cand * sl2);
           const uint64_t negm2 = f2_make(neg, neg);
           o_move = alpha;
-          if (vmax > vref) {
-            o_move *= vref / vmax;
-            vref = vmax;
+          float unit;
+          uint32_t far;
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=f"(unit), "=r"(far) : "r"(sc + 64));
+          if (unit != vref) {
+            o_move *= vref / unit;
+            vref = unit;
           }
-          const float unit = kPagedPScale / vref;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {   // the MMA takes each half as soon as it is ready
             uint32_t sr[64], pk[32];
@@ -862,15 +894,18 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             scales4(4 * h, ks);
             scales4(8 + 4 * h, vs);
             load64(h, sr);
+            auto weigh = [&](auto far_) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float kf = ks[e >> 3] * sl2, vf = vs[e >> 3] * unit;   // 8 pairs: one group
-              const uint64_t pp = exp2_pair(sr[2 * e], sr[2 * e + 1], f2_make(kf, kf), negm2);
-              rs2 = f2_add(rs2, pp);
-              float p0, p1;
-              f2_split(f2_mul(pp, f2_make(vf, vf)), p0, p1);
-              pk[e] = pack_f16x2(p0, p1);
-            }
+              for (int e = 0; e < 32; ++e) {
+                const float kf = ks[e >> 3] * sl2, vf = vs[e >> 3];   // 8 pairs: one group
+                const uint64_t pp = exp2_pair(sr[2 * e], sr[2 * e + 1], f2_make(kf, kf), negm2);
+                rs2 = f2_add(rs2, pp);
+                float p0, p1;
+                f2_split(decltype(far_)::value ? pp : f2_mul(pp, f2_make(vf, vf)), p0, p1);
+                pk[e] = decltype(far_)::value ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              }
+            };
+            if (far) weigh(Int<1>()); else weigh(Int<0>());
             hand_over(h, pk);
           }
         } else {
