@@ -81,6 +81,7 @@ struct PagedUnit {
     return unit != was;
   }
 };
+constexpr float kPagedLeastScale = 1.4e-45f;   // 2^-149: a score scale that underflows to 0 makes NaN of a masked score, -inf
 constexpr float kPagedLn2 = 0.69314718055994530942f;
 
 struct PagedParams {
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(32 * PagedLayout<D, FP8, NG>::WARPS, 1) fa_pag
           const int e = min(max(int(__float_as_uint(mx) >> 23) - 127, -100), 127);
           const bool scaled = mx > 0.f && mx < INFINITY;
           const float up = scaled ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : 1.f;    // 2^(14 - e)
-          rs *= scaled ? __uint_as_float(uint32_t(127 - 14 + e) << 23) : 1.f;
+          rs = fmaxf(rs * (scaled ? __uint_as_float(uint32_t(127 - 14 + e) << 23) : 1.f), kPagedLeastScale);
 #pragma unroll
           for (int c = 0; c < C; ++c) {
             qf[ng][c][0] = pack_f16x2(__uint_as_float(w2[c].x << 16) * up, __uint_as_float(w2[c].x & 0xffff0000u) * up);

@@ -173,7 +173,8 @@ __device__ __forceinline__ void wide_split_queries(const WideParams& q) {
     if (!real) continue;
     *reinterpret_cast<uint2*>(q.q8 + row * D + 8 * c) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2*>(q.q8 + (rows + row) * D + 8 * c) = make_uint2(lo[0], lo[1]);
-    if (c == 0) q.q_scale[row] = q.p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 7 + ex) << 23) : 1.f);
+    if (c == 0)
+      q.q_scale[row] = fmaxf(q.p.scale_log2 * (scaled ? __uint_as_float(uint32_t(127 - 7 + ex) << 23) : 1.f), kPagedLeastScale);
   }
 }
 
@@ -897,7 +898,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             auto weigh = [&](auto far_) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float kf = ks[e >> 3] * sl2, vf = vs[e >> 3];   // 8 pairs: one group
+                const float kf = fmaf(ks[e >> 3], sl2, kPagedLeastScale), vf = vs[e >> 3];   // 8 pairs: one group
                 const uint64_t pp = exp2_pair(sr[2 * e], sr[2 * e + 1], f2_make(kf, kf), negm2);
                 rs2 = f2_add(rs2, pp);
                 float p0, p1;
