@@ -508,7 +508,7 @@ PagedSpace paged_space(int B, int Hkv, const PagedShape& s, int d, int sms) {
   w.plan = w.ml + up256(rows * 8);
   w.info = w.plan + up256(size_t(s.plan) * 4);
   w.redo = w.info + up256(size_t(B) * Hkv * s.tiles * 8);
-  w.q8 = w.redo + (s.wide ? up256(size_t(B) * Hkv * s.tiles * 4) : 0);
+  w.q8 = w.redo + (s.wide ? up256((size_t(B) * Hkv * s.tiles + 1) * 4) : 0);
   w.q_scale = w.q8 + (s.wide ? up256(size_t(B) * Hkv * s.R * d * 2) : 0);
   w.total = w.q_scale + (s.wide ? up256(size_t(B) * Hkv * s.R * 4) : 0);
   return w;
@@ -631,7 +631,7 @@ fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cud
   st = launch_dependent<fa::WideParams>(fa::fa_paged_wide_combine_kernel<D>, pairs * fa::kWideMergeCtas, 256, 0, s,
                                         "fa_fwd_paged combine kernel launch", q);
   if (st != FA_OK || !p.causal || p.Nq == 1) return st;
-  return launch_dependent<fa::WideParams>(fa::fa_paged_wide_redo_kernel<D>, pairs, 256, 0, s, "fa_fwd_paged redo kernel launch", q);
+  return launch_dependent<fa::WideParams>(fa::fa_paged_wide_redo_kernel<D>, unsigned(2 * sms), 256, 0, s, "fa_fwd_paged redo kernel launch", q);
 }
 
 template <int D>

@@ -37,7 +37,8 @@ struct WideParams {
   int n_pairs;    // tile pairs per (sequence, K/V head)
   uint8_t* q8;    // e4m3: [2][B, Hq, Nq, D]: the queries' e4m3 and e5m2 parts
   float* q_scale; // [B, Hq, Nq]: what they stand for, times the softmax scale
-  int* redo;      // [B, Hkv, n_pairs]: nonzero where the pair has to be computed anew
+  int* redo;      // [B, Hkv, n_pairs]: 1 where O is not finite under a causal mask, 2 where the pair has to be computed anew
+                  // for it; and one more: nonzero where any has
   uint64_t wait_ns;
 };
 
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const __grid_consta
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int total = q.p.B * q.n_pairs;
   if (tid == 0) carry = q.p.plan[0] = 0;
-  for (int i = tid; i < total * q.p.Hkv; i += 1024) q.redo[i] = 0;
+  for (int i = tid; i <= total * q.p.Hkv; i += 1024) q.redo[i] = 0;
   __syncthreads();
   for (int base = 0; base < total; base += 1024) {
     const int at = base + tid;
@@ -1020,53 +1021,105 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
-// One query row by one warp, key by key: for pairs whose O is not finite.  There a value of V that is not
-// finite lies within the tiles, and the tensor core adds 0 * V = NaN to rows that do not see its key; here a row reads what
-// it sees and nothing else.  Rare, so only its result counts.
+// One query row by one warp, 32 keys at a time (a lane each for the scores, all lanes for each key's values): for pairs where
+// a value of V that is not finite lies behind the mask of some row.  There the tensor core adds 0 * V = NaN to rows
+// that do not see its key; here a row reads what it sees and nothing else.  sq: the warp's shared memory for the query.
 template <int D>
-__device__ __forceinline__ void paged_row(const PagedParams& p, int b, int h, int64_t row, int lim, int lane) {
+__device__ __forceinline__ void paged_row(const PagedParams& p, int b, int h, int64_t row, int lim, int lane, float* sq) {
   constexpr int PER = D / 32;
   const bool fp8 = p.k_scale != nullptr;
-  float q[PER], acc[PER];
+  float acc[PER];
+  __syncwarp();
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
-    q[e] = __bfloat162float(p.q[row * D + lane * PER + e]);
+    sq[lane * PER + e] = __bfloat162float(p.q[row * D + lane * PER + e]);
     acc[e] = 0.f;
   }
-  auto value = [&](const uint8_t* pool, int64_t at) {   // element `at` of a pool
-    if (!fp8) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[at]);
-    return __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(pool[at]) & 0xffffu)));
-  };
-  float m = -INFINITY, l = 0.f;
-  for (int pass = 0; pass < 2; ++pass)
-    for (int j = 0; j < lim; ++j) {
-      const int id = p.page_table[(int64_t)b * p.max_pages + (j >> p.page_shift)];
-      if (unsigned(id) >= unsigned(p.n_pages)) continue;   // (already reported)
-      const int64_t in = (((int64_t)h << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + lane * PER;
-      const uint8_t *k = p.k + uint64_t(id) * p.k_page_bytes, *v = p.v + uint64_t(id) * p.v_page_bytes;
-      float s = 0.f;
+  __syncwarp();
+  auto e4m3 = [](uint32_t code) { return __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(code) & 0xffffu))); };
+  float m = -INFINITY, l = 0.f;   // l: the lane's part
+  for (int j0 = 0; j0 < lim; j0 += 32) {
+    const int j = j0 + lane;
+    const int id = j < lim ? p.page_table[(int64_t)b * p.max_pages + (j >> p.page_shift)] : -1;
+    const bool seen = j < lim && unsigned(id) < unsigned(p.n_pages);   // (a page outside the pool has been reported)
+    const int64_t in = (((int64_t)h << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D;   // element of the key in its page
+    float s = 0.f, vs = 1.f;
+    if (seen) {
+      const uint8_t* k = p.k + uint64_t(id) * p.k_page_bytes;
+      if (fp8) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint2 w = *reinterpret_cast<const uint2*>(k + in + 8 * c);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) s = fmaf(q[e], value(k, in + e), s);
+          for (int e = 0; e < 8; ++e) s = fmaf(sq[8 * c + e], e4m3(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xffu), s);
+        }
+        s *= p.k_scale[(int64_t)id * p.Hkv + h];
+        vs = p.v_scale[(int64_t)id * p.Hkv + h];
+      } else {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(k + 2 * in + 16 * c);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int z = 16; z > 0; z >>= 1) s += __shfl_xor_sync(0xffffffffu, s, z);
-      s *= p.scale_log2 * (fp8 ? p.k_scale[(int64_t)id * p.Hkv + h] : 1.f);
-      if (pass == 0) {
-        m = fmaxf(m, s);
-        continue;
+          for (int e = 0; e < 8; ++e) s = fmaf(sq[8 * c + e], __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16), s);
+        }
       }
-      const float w = exp2f(s - m);
-      l += w;
-      const float vs = fp8 ? p.v_scale[(int64_t)id * p.Hkv + h] : 1.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, value(v, in + e) * vs, acc[e]);
+      s *= p.scale_log2;
     }
+    float mx = seen ? s : -INFINITY;
+#pragma unroll
+    for (int z = 16; z > 0; z >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+    mx = fmaxf(mx, m);
+    const float base = mx == -INFINITY ? 0.f : mx, a = exp2f(m - base), w = seen ? exp2f(s - base) : 0.f;
+    m = mx;
+    l = l * a + w;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= a;
+    const unsigned all = __ballot_sync(0xffffffffu, seen);
+#pragma unroll 4
+    for (int y = 0; y < 32; ++y) {
+      const float wy = __shfl_sync(0xffffffffu, w, y), vy = __shfl_sync(0xffffffffu, vs, y);
+      const int iy = __shfl_sync(0xffffffffu, id, y);
+      const int64_t at = __shfl_sync(0xffffffffu, in, y) + lane * PER;
+      if (!(all >> y & 1)) continue;
+      const uint8_t* v = p.v + uint64_t(iy) * p.v_page_bytes;
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        acc[e] = fmaf(wy, (fp8 ? e4m3(v[at + e]) : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(v)[at + e])) * vy, acc[e]);
+    }
+  }
+#pragma unroll
+  for (int z = 16; z > 0; z >>= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
 #pragma unroll
   for (int e = 0; e < PER; ++e) p.o[row * D + lane * PER + e] = __float2bfloat16_rn(l != 0.f ? acc[e] / l : 0.f);
   if (lane == 0) p.lse[row] = l != 0.f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
 }
 
+// Whether a value that is not finite lies among the keys that some row of the pair does not see: new tokens from the pair's first
+// position on, up to the end of its last block.  Elsewhere all rows see it, and O stands.  A whole CTA.  (Not inlined: that gave the
+// merge more registers and took 1 us of a call of 30.)
+template <int D>
+__device__ __noinline__ bool wide_hidden_value(const WideParams& q, int b, int h, int pair, int T) {
+  const PagedParams& p = q.p;
+  const int L = paged_key_len(p, b), lo = max(L - paged_new_len(p, b) + 2 * pair * q.tq + 1, 0), hi = min(L, T * 128);
+  const bool fp8 = p.k_scale != nullptr;
+  const int cpr = D / (fp8 ? 16 : 8);   // 16-byte chunks of a key
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int i = int(threadIdx.x); i < (hi - lo) * cpr; i += 256) {
+    const int j = lo + i / cpr, id = p.page_table[(int64_t)b * p.max_pages + (j >> p.page_shift)];
+    if (unsigned(id) >= unsigned(p.n_pages)) continue;
+    const int64_t row = ((int64_t)h << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+    const uint4 w = reinterpret_cast<const uint4*>(p.v + uint64_t(id) * p.v_page_bytes)[row * cpr + i % cpr];
+    bad |= fp8 ? not_finite<true>(w.x) | not_finite<true>(w.y) | not_finite<true>(w.z) | not_finite<true>(w.w)
+               : not_finite<false>(w.x) | not_finite<false>(w.y) | not_finite<false>(w.z) | not_finite<false>(w.w);
+  }
+  return __syncthreads_or(bad != 0);
+}
+
 // Merges the pairs that several CTAs shared and writes the rows of pairs without keys: a row per warp at a time,
-// 2 rows a warp (with 8, four CTAs a pair, latency kept it at 20 us on 256 pairs of 2 partials, 38 MB).
+// 2 rows a warp (with 8, four CTAs a pair, latency kept it at 20 us on 256 pairs of 2 partials, 38 MB).  Of a pair whose O is not
+// finite the first CTA finds out whether it has to be computed anew.
 constexpr int kWideMergeCtas = 16;
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid_constant__ WideParams q) {
@@ -1079,6 +1132,9 @@ __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid
   const int64_t at = (int64_t)b * q.n_pairs + pair;
   const bool has = p.plan[at + 1] > p.plan[at];
   const int2 info = p.info[item];
+  if (blockIdx.x % kWideMergeCtas == 0 && q.redo[item] != 0 &&
+      wide_hidden_value<D>(q, b, bh % p.Hkv, pair, p.plan[at + 1] - p.plan[at]) && threadIdx.x == 0)
+    q.redo[item] = 2, q.redo[p.B * p.Hkv * q.n_pairs] = 1;
   if (has && info.y < 0) return;
   const int rows = q.g * q.tq;   // of a tile
   for (int k = (blockIdx.x % kWideMergeCtas) * 8 + warp; k < 2 * rows; k += 8 * kWideMergeCtas) {
@@ -1091,21 +1147,30 @@ __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid
   }
 }
 
-// The pairs that have to be computed anew; one CTA a pair.  After the merge, and only under a causal mask.
+// The pairs that have to be computed anew, their rows spread over all warps of the grid.  After the merge, and only under a
+// causal mask.
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_wide_redo_kernel(const __grid_constant__ WideParams q) {
   const PagedParams& p = q.p;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const unsigned item = blockIdx.x;
-  if (q.redo[item] == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = item / q.n_pairs, pair = item % q.n_pairs, b = bh / p.Hkv;
-  const int rows = q.g * q.tq, L = paged_key_len(p, b), n = paged_new_len(p, b);
-  for (int k = warp; k < 2 * rows; k += 8) {
-    const int i = (2 * pair + k / rows) * q.tq + k % rows / q.g;
-    if (i >= p.Nq) break;
-    paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + k % rows % q.g) * p.Nq + i, i < n ? min(max(L - n + i + 1, 0), L) : 0, lane);
-  }
+  const int items = p.B * p.Hkv * q.n_pairs;
+  if (q.redo[items] == 0) return;
+  __shared__ float sq[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = int(gridDim.x) * 8, me = warp * int(gridDim.x) + int(blockIdx.x);
+  const int rows = q.g * q.tq;   // of a tile
+  int turn = 0;                  // the warp that takes the next pair's first row
+  for (int base = 0; base < items; base += 32)
+    for (unsigned flags = __ballot_sync(0xffffffffu, base + lane < items && q.redo[base + lane] == 2); flags != 0; flags &= flags - 1) {
+      const int item = base + __ffs(flags) - 1;
+      const int bh = item / q.n_pairs, pair = item % q.n_pairs, b = bh / p.Hkv;
+      const int L = paged_key_len(p, b), n = paged_new_len(p, b);
+      for (int k = me >= turn ? me - turn : me - turn + warps; k < 2 * rows; k += warps) {
+        const int i = (2 * pair + k / rows) * q.tq + k % rows / q.g;
+        if (i >= p.Nq) break;
+        paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + k % rows % q.g) * p.Nq + i, i < n ? min(max(L - n + i + 1, 0), L) : 0, lane, sq[warp]);
+      }
+      turn = (turn + 2 * rows) % warps;
+    }
 }
 
 }  // namespace fa
