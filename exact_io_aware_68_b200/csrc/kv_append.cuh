@@ -214,11 +214,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) f
   const int L = p.key_lens[b], n = p.new_lens == nullptr ? p.Nq : p.new_lens[b];
   const int page_size = 1 << p.page_shift;
   const long long cap = (long long)p.max_pages << p.page_shift;
-  if (n == 0) return;
-  if (n < 0 || n > p.Nq || L < n || L > cap || (p.cos != nullptr && L > p.max_pos)) {
+  if (n < 0 || n > p.Nq || L < n || L > cap || (p.cos != nullptr && L > p.max_pos && n > 0)) {
     record_status(kStatusRange);
     return;
   }
+  if (n == 0) return;
   const int start = L - n, pg = (start >> p.page_shift) + tp;
   const long long base = (long long)pg << p.page_shift;
   if (base >= L) return;
