@@ -120,6 +120,13 @@ fa_status check_common(int B, int H, int N, int d, float scale, float dropout_p,
     if (!aligned16(p)) return fail(FA_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p);     \
   } while (0)
 
+// The same for arrays that are only read 4 bytes at a time.
+#define FA_CHECK_WORDS(p)                                                                                      \
+  do {                                                                                                         \
+    if ((p) == nullptr) return fail(FA_ERR_INVALID_ARG, "%s is NULL", #p);                                     \
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return fail(FA_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p); \
+  } while (0)
+
 fa_status launch_status(const char* what) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -658,14 +665,15 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   FA_CHECK_PTR(v_cache);
   FA_CHECK_PTR(o);
   FA_CHECK_PTR(lse);
-  FA_CHECK_PTR(page_table);
-  FA_CHECK_PTR(key_lens);
+  FA_CHECK_WORDS(page_table);
+  FA_CHECK_WORDS(key_lens);
+  if (new_lens != nullptr) FA_CHECK_WORDS(new_lens);
   // (rows of q are read again after others' o is there, where a pair is computed anew)
   const uint64_t at_q = reinterpret_cast<uintptr_t>(q), at_o = reinterpret_cast<uintptr_t>(o), bytes = uint64_t(B) * Hq * Nq * d * 2;
   if ((at_o > at_q ? at_o - at_q : at_q - at_o) < bytes) return fail(FA_ERR_INVALID_ARG, "o overlaps q");
   if (fp8) {
-    FA_CHECK_PTR(k_scale);
-    FA_CHECK_PTR(v_scale);
+    FA_CHECK_WORDS(k_scale);
+    FA_CHECK_WORDS(v_scale);
   }
   if (workspace == nullptr) return fail(FA_ERR_INVALID_ARG, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -737,11 +745,12 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   FA_CHECK_PTR(k_cache);
   FA_CHECK_PTR(v_cache);
   if (fp8) {
-    FA_CHECK_PTR(k_scale);
-    FA_CHECK_PTR(v_scale);
+    FA_CHECK_WORDS(k_scale);
+    FA_CHECK_WORDS(v_scale);
   }
-  FA_CHECK_PTR(page_table);
-  FA_CHECK_PTR(key_lens);
+  FA_CHECK_WORDS(page_table);
+  FA_CHECK_WORDS(key_lens);
+  if (new_lens != nullptr) FA_CHECK_WORDS(new_lens);
   if (strides == nullptr) return fail(FA_ERR_INVALID_ARG, "strides is NULL");
   for (int i = q == nullptr ? 3 : 0; i < 9; ++i)
     if (strides[i] < 0 || strides[i] % 8 != 0)

@@ -189,6 +189,8 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  *    [B] or NULL (all Nq), how many of the step's Nq tokens are real, 0 <= new_lens[b] <= Nq.  New token
  *    i of sequence b stands at position key_lens[b] - new_lens[b] + i.  The same two arrays go to the
  *    append and to the attention.
+ *  - Alignment: 4 bytes for page_table, key_lens, new_lens, k_scale and v_scale (slices of larger arrays do),
+ *    256 for the workspace, 16 for everything else.
  *  - Grouped heads: query head h uses K/V head h / (Hq / Hkv); Hq must be a multiple of Hkv.
  *  - 1 <= B <= 4096, B * Hq <= 65535, Nq <= 2^20, and B * max_pages * page_size < 2^31.
  *  - What the device finds out of range (a page number outside [0, n_pages), key_lens outside
