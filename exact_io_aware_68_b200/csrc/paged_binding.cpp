@@ -37,6 +37,7 @@ bool fits(const Tensor& t, at::ScalarType dtype, at::IntArrayRef shape, int dev)
 
 struct Cache {
   int64_t n_pages, heads, page, width;
+  int64_t step[2];   // from page to page of k_cache, v_cache
   int dev;
   bool fp8;
 };
@@ -46,9 +47,11 @@ bool cache_fits(const Tensor& k, const Tensor& v, const Arg& ks, const Arg& vs, 
                 int64_t B, int64_t d, Cache& c) {
   if (!k.is_cuda() || !v.is_cuda() || k.dim() != 4 || k.size(3) != d || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type())
     return false;
-  c = Cache{k.size(0), k.size(1), k.size(2), 0, int(k.get_device()), k.scalar_type() == at::kFloat8_e4m3fn};
+  c = Cache{k.size(0), k.size(1), k.size(2), 0, {k.stride(0), v.stride(0)}, int(k.get_device()), k.scalar_type() == at::kFloat8_e4m3fn};
+  // (the stride of a dimension of size one is never taken)
   for (const Tensor* t : {&k, &v})
-    if (t->stride(1) != c.page * d || t->stride(2) != d || t->stride(3) != 1) return false;
+    if ((c.heads > 1 && t->stride(1) != c.page * d) || (c.page > 1 && t->stride(2) != d) || (d > 1 && t->stride(3) != 1)) return false;
+  if (c.n_pages == 1) c.step[0] = c.step[1] = c.heads * c.page * d;
   if (v.get_device() != c.dev || (!c.fp8 && k.scalar_type() != at::kBFloat16) || c.fp8 != (ks.t != nullptr) || c.fp8 != (vs.t != nullptr))
     return false;
   if (c.fp8 && !(fits(*ks.t, at::kFloat, {c.n_pages, c.heads}, c.dev) && fits(*vs.t, at::kFloat, {c.n_pages, c.heads}, c.dev))) return false;
@@ -95,10 +98,10 @@ PyObject* attention_call(PyObject* const* a, Py_ssize_t n) {
     fa_status st;
     Py_BEGIN_ALLOW_THREADS
     st = c.fp8 ? fa_fwd_paged_e4m3(q.ptr(), k.ptr(), v.ptr(), static_cast<const float*>(ks.ptr()), static_cast<const float*>(vs.ptr()),
-                                   out.data_ptr(), sums.data_ptr<float>(), k.t->stride(0), v.t->stride(0), pt, kl, nl, int(B), int(Hq),
+                                   out.data_ptr(), sums.data_ptr<float>(), c.step[0], c.step[1], pt, kl, nl, int(B), int(Hq),
                                    int(c.heads), int(Nq), int(d), int(c.n_pages), int(c.page), int(c.width), float(scale), causal,
                                    space.data_ptr(), size_t(space.numel()), stream)
-               : fa_fwd_paged(q.ptr(), k.ptr(), v.ptr(), out.data_ptr(), sums.data_ptr<float>(), k.t->stride(0), v.t->stride(0), pt, kl,
+               : fa_fwd_paged(q.ptr(), k.ptr(), v.ptr(), out.data_ptr(), sums.data_ptr<float>(), c.step[0], c.step[1], pt, kl,
                               nl, int(B), int(Hq), int(c.heads), int(Nq), int(d), int(c.n_pages), int(c.page), int(c.width),
                               float(scale), causal, space.data_ptr(), size_t(space.numel()), stream);
     Py_END_ALLOW_THREADS
@@ -162,10 +165,10 @@ PyObject* append_call(PyObject* const* a, Py_ssize_t n) {
     fa_status st;
     Py_BEGIN_ALLOW_THREADS
     st = c.fp8 ? fa_kv_append_e4m3(q.ptr(), k.ptr(), v.ptr(), strides, q_out, kc.ptr(), vc.ptr(), static_cast<float*>(ks.ptr()),
-                                   static_cast<float*>(vs.ptr()), kc.t->stride(0), vc.t->stride(0), pt, kl, nl, cp, sp, int(max_pos),
+                                   static_cast<float*>(vs.ptr()), c.step[0], c.step[1], pt, kl, nl, cp, sp, int(max_pos),
                                    int(2 * half), inter, int(B), int(Hq), int(Hkv), int(Nq), int(d), int(c.n_pages), int(c.page),
                                    int(c.width), stream)
-               : fa_kv_append(q.ptr(), k.ptr(), v.ptr(), strides, q_out, kc.ptr(), vc.ptr(), kc.t->stride(0), vc.t->stride(0), pt, kl,
+               : fa_kv_append(q.ptr(), k.ptr(), v.ptr(), strides, q_out, kc.ptr(), vc.ptr(), c.step[0], c.step[1], pt, kl,
                               nl, cp, sp, int(max_pos), int(2 * half), inter, int(B), int(Hq), int(Hkv), int(Nq), int(d),
                               int(c.n_pages), int(c.page), int(c.width), stream);
     Py_END_ALLOW_THREADS

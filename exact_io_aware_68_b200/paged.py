@@ -50,7 +50,8 @@ def _refuse_cache(k_cache, v_cache, k_scale, v_scale, page_table, key_lens, new_
           "[n_pages, Hkv, page_size, d], both the same")
     _need(shape[3] == d, f"the pools have d = {shape[3]}, the heads {d}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(t.stride()[1:] == (shape[2] * d, d, 1), f"{name} must be contiguous within a page")
+        _need(all(n == 1 or st == want for n, st, want in zip(shape[1:], t.stride()[1:], (shape[2] * d, d, 1))),
+              f"{name} must be contiguous within a page")
     _need((k_scale is not None) == fp8 and (v_scale is not None) == fp8, "k_scale and v_scale go with float8_e4m3fn pools")
     for name, t, dtype, sh in (("v_cache", v_cache, dt, shape), ("k_scale", k_scale, torch.float32, shape[:2]),
                                ("v_scale", v_scale, torch.float32, shape[:2]), ("key_lens", key_lens, torch.int32, (B,)),
