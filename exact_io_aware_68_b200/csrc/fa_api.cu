@@ -729,6 +729,15 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   return d == 64 ? launch_paged_rows<64>(q4, fp8, shape.rows, sms, s) : launch_paged_rows<128>(q4, fp8, shape.rows, sms, s);
 }
 
+// Bytes from the first element to the end of the last of a bf16 array [B, H, N, d] with element strides st (batch, head, token).
+uint64_t span_of(int B, int H, int N, int d, const int64_t* st) {
+  return 2 * (uint64_t(B - 1) * st[0] + uint64_t(H - 1) * st[1] + uint64_t(N - 1) * st[2] + d);
+}
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
 fa_status run_append(bool fp8, const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
                      void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t k_page_stride,
                      int64_t v_page_stride, const int32_t* page_table, const int32_t* key_lens, const int32_t* new_lens,
@@ -762,6 +771,15 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
     if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0)
       return fail(FA_ERR_UNSUPPORTED, "rot_dim = %d: a multiple of 16, at most d = %d", rot_dim, d);
     if (max_pos < 1) return fail(FA_ERR_INVALID_ARG, "max_pos = %d must be >= 1", max_pos);
+  }
+  if (q != nullptr) {   // a thread writes a query row where it read it; elsewhere another thread may not have read yet
+    const uint64_t out = 2 * uint64_t(B) * Hq * Nq * d;
+    const bool contiguous = (B == 1 || strides[0] == int64_t(Hq) * Nq * d) && (Hq == 1 || strides[1] == int64_t(Nq) * d) &&
+                            (Nq == 1 || strides[2] == d);
+    if (!(q_out == q && contiguous) && overlap(q_out, out, q, span_of(B, Hq, Nq, d, strides)))
+      return fail(FA_ERR_INVALID_ARG, "q_out overlaps q");
+    if (overlap(q_out, out, k, span_of(B, Hkv, Nq, d, strides + 3)) || overlap(q_out, out, v, span_of(B, Hkv, Nq, d, strides + 6)))
+      return fail(FA_ERR_INVALID_ARG, "q_out overlaps k or v");
   }
   fa::AppendParams p{};
   const void* x[3] = {q, k, v};

@@ -86,7 +86,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, key_lens, new_lens=None, rope=
     contiguous (views of a projection's output need no copy).  rope: (cos, sin) tables, applied to k and q by position
     (``rope_tables``); interleaved: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Writes the pools (and
     the scales of e4m3 pools) in place; returns the rotated queries, contiguous [B, Hq, Nq, d], or None.  q_out: where
-    to write those; a contiguous q itself, or no memory of q's."""
+    to write those; a contiguous q itself, or no memory of q's, k's or v's."""
     cos, sin = (None, None) if rope is None else rope
     out = _binding().append(k, v, k_cache, v_cache, page_table, key_lens, new_lens, cos, sin, interleaved, q, k_scale, v_scale, q_out)
     if out is True:

@@ -203,8 +203,8 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  * q, k, v: bf16 [B, Hq | Hkv | Hkv, Nq, d] with d contiguous; strides: HOST array of nine element strides
  * (batch, head, token of q, then k, then v), multiples of 8, so that views of one projection output need
  * no copy.  q may be NULL (then q_out is not written); q_out: bf16 [B, Hq, Nq, d] contiguous (a contiguous q
- * itself, or without overlap), rows of queries that are no token (i >= new_lens[b]) are set to 0.  Rows of the pool that get no token keep
- * their bytes.
+ * itself; refused where it overlaps q, k or v otherwise), rows of queries that are no token (i >= new_lens[b]) are
+ * set to 0.  Rows of the pool that get no token keep their bytes.
  * Rotation: rope_cos, rope_sin fp32 [max_pos, rot_dim / 2], both NULL for none; rot_dim a multiple of
  * 16, at most d; features past rot_dim pass through.  Pair (x, y) becomes (x cos - y sin,
  * y cos + x sin) in fp32, products rounded before the sum, pairs (i, i + rot_dim / 2), or (2i, 2i + 1)
