@@ -812,6 +812,8 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
   p.n_pages = n_pages;
   p.page_shift = log2_of(page_size);
   p.max_pages = max_pages;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != FA_OK) return st;
   const int heads = p.Hq + (fp8 ? 0 : 2 * Hkv);
   const int64_t tokens = int64_t(B) * Nq;
   // the row role's blocks hold `threads` threads of d / 16 per token; a thread takes up to 8 heads of its token
@@ -820,7 +822,7 @@ fa_status run_append(bool fp8, const void* q, const void* k, const void* v, cons
     const int per = threads / (d / 16);
     const int64_t x = (tokens + per - 1) / per;
     p.heads_per_thread = 1;
-    while (p.heads_per_thread < 8 && tokens * (d / 16) * heads / (2 * p.heads_per_thread) >= 148 * 2048) p.heads_per_thread *= 2;
+    while (p.heads_per_thread < 8 && tokens * (d / 16) * heads / (2 * p.heads_per_thread) >= int64_t(sms) * 2048) p.heads_per_thread *= 2;
     const int64_t blocks = heads == 0 ? 0 : x * ((heads + p.heads_per_thread - 1) / p.heads_per_thread);
     p.row_blocks_x = int(x);
     p.row_blocks = int(blocks);
