@@ -610,8 +610,9 @@ fa_status make_group_map(CUtensorMap* map, const void* ptr, bool bits8, int d, i
 }
 
 template <int D, bool FP8>
-fa_status launch_paged_wide(const fa::WideParams& q, int page_size, int sms, cudaStream_t s) {
+fa_status launch_paged_wide(fa::WideParams q, int page_size, int sms, cudaStream_t s) {
   using L = fa::WideLayout<D, FP8>;
+  q.p.n_warps = paged_ctas(sms);
   CUtensorMap mq, mq2, mk, mv;
   fa_status st;
   const fa::PagedParams& p = q.p;
@@ -722,6 +723,7 @@ fa_status run_paged(bool fp8, const void* q, const void* k_cache, const void* v_
   q4.q8 = reinterpret_cast<uint8_t*>(ws + space.q8);
   q4.q_scale = reinterpret_cast<float*>(ws + space.q_scale);
   q4.wait_ns = g_wait_ns.load();
+  q4.debug_flags = g_debug_flags.load();
   if (shape.wide) {
     if (d == 64) return fp8 ? launch_paged_wide<64, true>(q4, page_size, sms, s) : launch_paged_wide<64, false>(q4, page_size, sms, s);
     return fp8 ? launch_paged_wide<128, true>(q4, page_size, sms, s) : launch_paged_wide<128, false>(q4, page_size, sms, s);

@@ -102,7 +102,7 @@ struct PagedParams {
   uint32_t k_page_bytes, v_page_bytes;   // from one page to the next
   int B, Hkv, Nq, R, row_tiles;         // R = rows per K/V head
   int n_pages, page_shift, max_pages;
-  int n_warps;                 // of the whole grid
+  int n_warps;                 // of the whole grid (wide path: CTAs): how many hold partials
   int causal;
   float scale_log2;
 };

@@ -40,6 +40,7 @@ struct WideParams {
   int* redo;      // [B, Hkv, n_pairs]: 1 where O is not finite under a causal mask, 2 where the pair has to be computed anew
                   // for it; and one more: nonzero where any has
   uint64_t wait_ns;
+  int debug_flags;   // bit 2: the K producer never delivers the first block (exercises the timeout path)
 };
 
 // A segment: consecutive blocks of one pair, as much of it as falls into the CTA's share.
@@ -483,6 +484,7 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const int key0 = (s.t + j) * 128;
           const bool ends = !FP8 && !is_k && key0 + 128 > s.L;
           if (!__all_sync(0xffffffffu, g < NS || mbar_wait(&empty[st], ((g / NS) - 1) & 1, wc))) { ok = false; break; }
+          if (is_k && g == 0 && (q.debug_flags & 4)) { ok = false; break; }   // test hook
           uint64_t* bar = ends ? tail : &full[st];
           if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * piece_rows * (FP8 ? D : 2 * D));
           __syncwarp();
@@ -1136,13 +1138,15 @@ __global__ void __launch_bounds__(256) fa_paged_wide_combine_kernel(const __grid
       wide_hidden_value<D>(q, b, bh % p.Hkv, pair, p.plan[at + 1] - p.plan[at]) && threadIdx.x == 0)
     q.redo[item] = 2, q.redo[p.B * p.Hkv * q.n_pairs] = 1;
   if (has && info.y < 0) return;
+  // (a CTA whose wait ran out leaves what the workspace held: then no slot may be taken from it)
+  const bool found = has && unsigned(info.x) < 2u * p.n_warps && info.y < p.n_warps;
   const int rows = q.g * q.tq;   // of a tile
   for (int k = (blockIdx.x % kWideMergeCtas) * 8 + warp; k < 2 * rows; k += 8 * kWideMergeCtas) {
     const int x = k >= rows ? 1 : 0, r = k - x * rows;
     const int i = (2 * pair + x) * q.tq + r / q.g;
     if (i >= p.Nq) break;
     PagedMerge<D / 32> a;
-    if (has) a.template gather<2>(p, info, 0, 1, 256, 128 * x + r, lane);
+    if (found) a.template gather<2>(p, info, 0, 1, 256, 128 * x + r, lane);
     a.store(p, ((int64_t)bh * q.g + r % q.g) * p.Nq + i, lane);
   }
 }

@@ -287,8 +287,9 @@ FA_API const char* fa_get_error(void);
 FA_API void fa_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook.  Bit 0: the forward's load warp never delivers its first K/V block; bit 1: the
- * backward's load warp never delivers its first Q tile.  Either way the consumers' bounded waits
- * run out, the kernel unwinds and fa_check() returns FA_ERR_TIMEOUT.  0 = normal. */
+ * backward's load warp never delivers its first Q tile; bit 2: the paged attention's wide kernel never
+ * gets its first block of K.  Each way the consumers' bounded waits run out, the kernel unwinds and
+ * fa_check() returns FA_ERR_TIMEOUT.  0 = normal. */
 FA_API void fa_debug_set_flags(int flags);
 
 /* Library version string. */
