@@ -6,10 +6,10 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
-#include <exception>
 
 #include "../../include/fa.h"
 
@@ -178,17 +178,12 @@ PyObject* append_call(PyObject* const* a, Py_ssize_t n) {
   }
 }
 
-// No C++ exception leaves the module (out of memory, or a tensor without storage).
+// No C++ exception leaves the module: torch's own become what torch raises for them (OutOfMemoryError and the like).
 template <PyObject* (*CALL)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  try {
-    return CALL(a, n);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
-  }
-  return nullptr;
+  HANDLE_TH_ERRORS
+  return CALL(a, n);
+  END_HANDLE_TH_ERRORS
 }
 
 PyMethodDef methods[] = {
