@@ -28,11 +28,11 @@
 //  * 12 warps of 168 registers for 8 rows, 8 warps of 255 beyond, with rings of two tiles of 8 KB: what spills least.  Shared
 //    memory is taken from L1, and where it takes nearly all of it a spilled register is a trip to L2: a third tile
 //    costs 20 rows of D = 128 48.2 against 45.3 us in bf16, and gains nothing elsewhere (16 rows 58.2 against 57.7).
-//    Tiles of 4 KB where an e4m3 tile's scores would not fit into the registers beside O: 32 rows of D = 64 39.4 -> 33.0 us,
-//    24 of D = 128 49.3 -> 45.2 us (16 rows, where they fit, 48 -> 56 us).
-// Measured (B200, the whole call, 32/8 heads, D = 128): 64 sequences of 100 to 4000 keys, one query each, 89 us in bf16
-// (6.05 TB/s of K and V, 92 % of the copy rate) and 56 us in e4m3 (4.8 TB/s; there the warps' own latency bounds:
-// issue slots 44 % used, waits on memory rare); 16 heads x 65,536 keys, 8 queries, 91 us (5.9 TB/s); 8 x 32,768 keys
+//    Tiles of 4 KB where an e4m3 tile's scores would not fit into the registers beside O: 32 rows of D = 64 39.4 -> 33.0 us (34.8
+//    since scales may lie far apart), 24 of D = 128 49.3 -> 45.2 us (44; 16 rows, where they fit, 48 -> 56 us).
+// Measured (B200, the whole call, 32/8 heads, D = 128): 64 sequences of 100 to 4000 keys, one query each, 90 us in bf16
+// (6.0 TB/s of K and V, 91 % of the copy rate) and 57 us in e4m3 (4.7 TB/s; there the warps' own latency bounds:
+// issue slots 47 % used, waits on memory rare); 16 heads x 65,536 keys, 8 queries, 91 us (5.9 TB/s); 8 x 32,768 keys
 // e4m3, 64/8 heads, 93 us (5.8 TB/s).  About 10 us of a call are launch, look-ups, first loads and the merge.
 // Tried and slower: tiles of 2 KB with 14 to 16 warps (57 -> 60 us e4m3), a loop over 16-key groups in place of unrolled
 // tiles (57 -> 58 us), a 16-row tile with untransposed products (102 us e4m3), S by 8-bit MMAs with queries of two 8-bit parts

@@ -17,11 +17,12 @@
 //    is turned into f16 (exact; NaN stays NaN) by four more warps, in the swizzled layout the MMA reads.  The
 //    page's key scale multiplies the finished scores, its value scale the probabilities; where value scales lie far apart
 //    (PagedUnit) a block's P and V are bf16, with V times its scale.
-// Measured (B200, the whole call): 4 sequences, 512 new tokens against 4097 to 8100 keys, 32/8 heads, D = 128, causal:
-// 184 us in bf16 (1010 TFLOP/s, 0.62 of the measured cuBLAS burst rate; tensor pipe active 56 %, as in the training
-// forward: the chain S, softmax, PV of the tiles bounds), 3 x 256 new tokens in e4m3 102 us (630 TFLOP/s; tensor
-// pipe 37 %).  A clock trace of the latter shows 4200 cycles a unit in the steady state (bf16: 3750) and about 10,000 at
-// every change of segment, where code that has left the instruction cache runs: hence the rolled loops there.
+// Measured (B200, the whole call): 4 sequences, 512 new tokens against 4097 to 8100 keys, 32/8 heads, D = 128, causal: 187 us in
+// bf16 in a short run (1000 TFLOP/s, 0.61 of the measured cuBLAS burst rate; tensor pipe active 55 %, as in the training
+// forward: the chain S, softmax, PV of the tiles bounds) and 218 us (850 TFLOP/s) in a long one, where the power cap lowers
+// the clock; 3 x 256 new tokens in e4m3 103 us (630 TFLOP/s; tensor pipe 36 %).  A clock trace of the latter shows 4200 cycles
+// a unit in the steady state (bf16: 3750) and about 10,000 at every change of segment, where code that has left the
+// instruction cache runs: hence the rolled loops there.
 // Tried and slower: both tiles on alternating key blocks of one 128-row tile (75 -> 81 us for 64 rows, bf16); V and K both
 // converted to f16 (205 us where 8-bit K takes 146); the queries converted by this kernel's warps (4 us a tile).
 #pragma once
@@ -567,7 +568,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             uint32_t id_pv = kIdPV;
             if (j >= 0) {   // far: bf16
               uint32_t far;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(far) : "r"(smem_u32(smem) + L::SC_OFF + (gk + j) % L::SST * L::SET + 68) : "memory");
+              const uint32_t at = smem_u32(smem) + L::SC_OFF + (gk + j) % L::SST * L::SET + 68;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(far) : "r"(at) : "memory");
               if (far) id_pv |= kType;
             }
             bool have_k = false;   // K_{j+1} resident
@@ -686,7 +688,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // are masked), looked up one block ahead, their pages two blocks
       auto group_page = [&](int j) -> int {
         const int key = (s.t + j) * 128 + 16 * (lane & 7);
-        return lane < 16 && (warp == 12 || lane >= 8) && j < n_max && key < s.L ? global_load(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
+        const bool mine = lane < 16 && (warp == 12 || lane >= 8) && j < n_max && key < s.L;
+        return mine ? global_load(p.page_table + (int64_t)s.b * p.max_pages + (key >> p.page_shift)) : -1;
       };
       auto group_scale = [&](int id) -> float {
         if (unsigned(id) >= unsigned(p.n_pages)) return lane < 8 ? 1.f : 0.f;
@@ -706,7 +709,8 @@ fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const bool value = lane >= 8 && my_scale > 0.f;
         if (__any_sync(0xffffffffu, value && (my_scale > vu.unit || my_scale < vu.least))) {
           const uint32_t bits = __float_as_uint(my_scale);   // (positive floats order as their bits do)
-          const uint32_t hi = __reduce_max_sync(0xffffffffu, value ? bits : 0u), lo = __reduce_min_sync(0xffffffffu, value ? bits : 0x7f800000u);
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, value ? bits : 0u);
+          const uint32_t lo = __reduce_min_sync(0xffffffffu, value ? bits : 0x7f800000u);
           float move;
           vu.meet(__uint_as_float(hi), __uint_as_float(lo), move);
           unit = kPagedPScale / vu.unit;
@@ -1171,7 +1175,8 @@ __global__ void __launch_bounds__(256) fa_paged_wide_redo_kernel(const __grid_co
       for (int k = me >= turn ? me - turn : me - turn + warps; k < 2 * rows; k += warps) {
         const int i = (2 * pair + k / rows) * q.tq + k % rows / q.g;
         if (i >= p.Nq) break;
-        paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + k % rows % q.g) * p.Nq + i, i < n ? min(max(L - n + i + 1, 0), L) : 0, lane, sq[warp]);
+        const int lim = i < n ? min(max(L - n + i + 1, 0), L) : 0;
+        paged_row<D>(p, b, bh % p.Hkv, ((int64_t)bh * q.g + k % rows % q.g) * p.Nq + i, lim, lane, sq[warp]);
       }
       turn = (turn + 2 * rows) % warps;
     }

@@ -238,9 +238,10 @@ FA_API fa_status fa_kv_append_e4m3(const void* q, const void* k, const void* v, 
  * A query with no key, and one that is no token (i >= new_lens[b]), gets O = 0 and lse = -inf.
  * workspace: at least fa_fwd_paged_workspace_size() bytes (of the current device; with no visible
  * device a size that is enough on any), 256-byte aligned, clobbered; not shared by calls that may
- * overlap.  Its size does not depend on the sequences' lengths.  Two kernel launches, or (more than 24 query rows
- * per K/V head, 32 at d = 64) three, four with causal != 0.  A value of K or V that is not finite reaches the
- * queries that see its key, and no other. */
+ * overlap.  Its size does not depend on the sequences' lengths.  Two kernel launches; more than 24 query rows per
+ * K/V head (32 at d = 64) take three, and four with causal != 0 and Nq > 1, unless the group has more than 128 heads.
+ * A value of K or V that is not finite reaches the queries that see its key, and no other (where it is
+ * hidden from a query of a four-launch call, those around it are computed anew, which takes milliseconds). */
 FA_API size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
 FA_API fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
                        int64_t k_page_stride, int64_t v_page_stride, const int32_t* page_table,
