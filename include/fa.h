@@ -180,7 +180,7 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  *    contiguous, consecutive pages k_page_stride / v_page_stride elements apart (a multiple of 16, at
  *    least Hkv * page_size * d, below 2^31; larger where one allocation holds several pools).  bf16, or e4m3 with
  *    one fp32 scale per page and head: k_scale, v_scale [n_pages, Hkv]; a stored code c means c * scale.
- *    Scales are finite and > 0, as far apart as they like (keys below 2^100; of values, what is below 2^-93 loses bits
+ *    Scales are finite and > 0, as far apart as they like (keys and values below 2^100; a value below 2^-93 loses bits
  *    where scales lie more than 2^8 apart).  page_size in {16, 32, 64, 128, 256}; d in {64, 128}.
  *  - page_table: int32 [B, max_pages].  Key j of sequence b is row j % page_size of page
  *    page_table[b][j / page_size].  Entries past a sequence's last key are not read.  Pages may be
